@@ -537,6 +537,122 @@ MOE_API moe_status moe_unpermute_combine(const void *Y, int y_dtype, const int32
                                          moe_stream_t stream);
 
 /* ======================================================================== */
+/* 16-bit weights: the linear, and the layer with bf16 experts               */
+/* ======================================================================== */
+/*
+ * The unquantised side of a model with 4-bit experts: the dense linears (the
+ * shared expert's and the projections'), and the same MoE layer with its
+ * experts kept in bf16.  Sources: the bf16 tensors beside the quantised ones
+ * ("Drama 3 - NVFP4 routed experts", section "Quantization"; "drama-3-w4a16",
+ * table "At a glance"), and the bf16 experts that the quantised ones are
+ * compared with ("Drama 3 - NVFP4 routed experts", "Validation and
+ * listening").  Weights are used as a checkpoint stores them (row-major,
+ * [out][in]); nothing is packed.
+ */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1, MOE_F16 = 2 } moe_dtype;
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1,      /* v / (1 + exp(-v)) */
+  MOE_ACT_GELU = 2,      /* v (1 + erf(v / sqrt 2)) / 2 */
+  MOE_ACT_GELU_TANH = 3, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+  MOE_ACT_RELU = 4,      /* max(v, 0) */
+  MOE_ACT_SIGMOID = 5    /* 1 / (1 + exp(-v)) */
+} moe_act;
+
+/*
+ * The linear with its epilogue, for x [T][K] and w [rows][K]:
+ *   gated = 0:  y = act(x w^T + bias) + residual              rows = N
+ *   gated = 1:  y = act(g) * u + residual, (g, u) = x w^T + bias,
+ *               rows = 2N: rows [0, N) of w and bias give g, [N, 2N) give u
+ * Products and sums are fp32 in an order fixed by the sizes (the same call
+ * gives the same bits), the epilogue is fp32, and y is rounded once.
+ * x, w, bias [rows] and residual [T][N] are of `dtype` (MOE_BF16 or MOE_F16),
+ * y [T][N] of `y_dtype` (`dtype` or MOE_F32); bias and residual may be NULL.
+ * ldx, ldw, ldr, ldy: elements from one row to the next, at least the row's
+ * length; a row's tail past its length is neither used nor written (the 16-byte
+ * block that a row of x or w ends in may be read).
+ * y may be the residual itself (same address, type and row stride); beyond
+ * that no output may overlap an input.
+ * Requirements: x and w 16-byte aligned, ldx % 8 == 0 and ldw % 8 == 0, N <=
+ * 2^30, row strides below 2^38; any T, N, K.  T == 0 or N == 0 is a no-op.
+ * No workspace.  Errors: INVALID_ARG (null, a negative size, K == 0, an unknown type
+ * or activation, a row stride below its row's length, misalignment),
+ * UNSUPPORTED_SHAPE, CUDA.
+ */
+MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, int T, int N,
+                              int K, int dtype, const void *bias, int act, int gated,
+                              const void *residual, int64_t ldr, void *y, int64_t ldy, int y_dtype,
+                              moe_stream_t stream);
+
+/*
+ * One MoE layer's bf16 experts, experts back to back, all in device memory:
+ *   gate_up bf16 [E][2F][H]: rows [0, F) gate, rows [F, 2F) up
+ *   down    bf16 [E][H][F]
+ * A HOST struct read during the call only.
+ */
+typedef struct {
+  int E, H, F;
+  const uint16_t *gate_up;
+  const uint16_t *down;
+} moe_bf16_layer;
+
+/*
+ * One whole MoE layer with bf16 experts for a small batch:
+ *   logits[t][e] = sum_c x[t][c] wr[e][c]            (wr bf16 [Er][H] given), or
+ *   logits fp32 [T][Er] as given                      (wr NULL);
+ *   idx, w = the routing of moe_route on those logits;
+ *   row(t, e) = W_down,e (SiLU(W_gate,e x[t]) * W_up,e x[t])            (fp32)
+ *   y[t] = bf16( sum over j < k, ascending, of w[t][j] row(t, idx[t][j])
+ *                + s[t] row(t, shared) + residual[t] )
+ * shared = 1: `layer` holds Er + 1 experts, the last one shared by every
+ * token with s = 1, or s = sigmoid(sum_c x[t][c] shared_gate[c]) when
+ * shared_gate (bf16 [H]) is given.  shared = 0: Er = layer->E, no such term,
+ * shared_gate NULL.  residual: bf16 [T][H] or NULL.
+ * x, y bf16 [T][H].  logits: the input when wr is NULL, else an optional
+ * output; idx [T][k], w [T][k]: optional outputs (both or neither).  y may be
+ * the residual itself; beyond that no output may overlap an input.
+ * Each selected expert's weights are read once per call whatever the number
+ * of tokens routed to it; sums are fp32 in a fixed order; h enters the down
+ * projection with 16 significant bits or more (the int4 layer rounds it to
+ * bf16's 8).  Source: the passages of moe_decode_layer_w4a16_router; the gate
+ * on the shared expert is the Qwen3.5-MoE backbone's.
+ * Workspace: moe_decode_layer_bf16_workspace_bytes(T, k, shared, E, H, F) (E =
+ * layer->E) bytes, 16-byte aligned, zero-filled before its first use,
+ * reusable by stream-ordered calls and replayed graphs; calls that share a
+ * workspace must not overlap in time.  After a call that raised the device
+ * error word, zero-fill it again.  Co-residency as for moe_ffn_w4a16_decode.
+ * Limits: 0 <= T <= 16, T * (k + shared) <= 256, 1 <= k <= min(Er, 32), k +
+ * shared <= 32, E <= 1024, H % 64 == 0, F % 64 == 0.  Pointers to bf16
+ * 16-byte aligned.  T == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * WORKSPACE, CUDA.  A wait on the device that runs out raises
+ * MOE_DEVERR_DECODE_H_WAIT or MOE_DEVERR_DECODE_ROUTER_WAIT.
+ */
+MOE_API size_t moe_decode_layer_bf16_workspace_bytes(int T, int k, int shared, int E, int H, int F);
+MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer, const uint16_t *x,
+                                         const uint16_t *wr, float *logits, int T, int k, int shared,
+                                         const uint16_t *shared_gate, const uint16_t *residual,
+                                         uint16_t *y, int32_t *idx, float *w, void *ws, size_t ws_bytes,
+                                         moe_stream_t stream);
+
+/*
+ * Prefill with bf16 experts: moe_ffn_grouped_prefill on unquantised weights.
+ * x_perm bf16 [rows][H] grouped by expert, offsets [E+1] (device) from
+ * moe_permute; y_perm bf16 [rows][H] = W_down h, h = bf16(SiLU(W_gate x) *
+ * W_up x), fp32 sums.  A shared expert runs as expert E of a layer of E + 1
+ * (moe_route_shared, moe_permute).  Entries of offsets outside [0, rows] are
+ * clamped; rows that no expert owns are left as they were.
+ * Workspace: moe_prefill_bf16_workspace_bytes(rows, F) bytes, 16-byte
+ * aligned; after the call its first rows * F * 2 bytes hold h (bf16 [rows][F]).
+ * Requirements: H % 64 == 0, F % 64 == 0, E <= 1024, offsets non-decreasing
+ * with offsets[0] == 0 and offsets[E] == rows; pointers 16-byte aligned.
+ * rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, WORKSPACE, CUDA.
+ */
+MOE_API size_t moe_prefill_bf16_workspace_bytes(int rows, int F);
+MOE_API moe_status moe_ffn_grouped_prefill_bf16(const moe_bf16_layer *layer, const uint16_t *x_perm,
+                                                const int32_t *offsets, int rows, uint16_t *y_perm,
+                                                void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ======================================================================== */
 /* Device error word                                                         */
 /* ======================================================================== */
 /* Host pointer out receives (after a stream synchronise done by this call)

@@ -22,6 +22,8 @@ MOE_ERR_WORKSPACE, MOE_ERR_CUDA, MOE_ERR_TIMEOUT = 3, 4, 5
 MOE_DEVERR_DECODE_H_WAIT, MOE_DEVERR_PREFILL_WAIT = 0x101, 0x201
 MOE_DEVERR_DECODE_ROUTER_WAIT = 0x102
 MOE_W4_PLAIN, MOE_W4_GATE_UP = 0, 1
+MOE_BF16, MOE_F32, MOE_F16 = 0, 1, 2
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_SIGMOID = range(6)
 
 _lib = None
 
@@ -47,7 +49,12 @@ class moe_nvfp4_layer(ctypes.Structure):
                 ("g_gu", ctypes.c_void_p), ("g_d", ctypes.c_void_p)]
 
 
-_vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+class moe_bf16_layer(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("H", ctypes.c_int), ("F", ctypes.c_int),
+                ("gate_up", ctypes.c_void_p), ("down", ctypes.c_void_p)]
+
+
+_vp, _i, _sz, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [_i]),
     "moe_last_error_string": (ctypes.c_char_p, []),
@@ -92,6 +99,12 @@ SIGNATURES = {
     "moe_ffn_grouped_prefill_nvfp4": (_i, [ctypes.POINTER(moe_nvfp4_layer), _vp, _vp, _vp, _vp, _i, _vp, _vp, _sz,
                                            _vp]),
     "moe_unpermute_combine": (_i, [_vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp]),
+    "moe_linear": (_i, [_vp, _i64, _vp, _i64, _i, _i, _i, _i, _vp, _i, _i, _vp, _i64, _vp, _i64, _i, _vp]),
+    "moe_decode_layer_bf16_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "moe_decode_layer_bf16": (_i, [ctypes.POINTER(moe_bf16_layer), _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _sz, _vp]),
+    "moe_prefill_bf16_workspace_bytes": (_sz, [_i, _i]),
+    "moe_ffn_grouped_prefill_bf16": (_i, [ctypes.POINTER(moe_bf16_layer), _vp, _vp, _i, _vp, _vp, _sz, _vp]),
     "moe_device_error": (_i, [ctypes.POINTER(ctypes.c_int), _vp]),
     "moe_debug_starve_decode": (_i, [ctypes.POINTER(moe_w4_layer), _vp, _vp, _i, _i, _vp, _vp, _sz, ctypes.c_uint,
                                      _vp]),
@@ -352,6 +365,76 @@ def moe_unpermute_combine(Y, w, y, inv=None, stream=None):
     y_dtype = 0 if Y.element_size() == 4 else 1
     _check(lib().moe_unpermute_combine(_p(Y), y_dtype, _p(inv), _p(w), T, k, H, _p(y),
                                        _stream(stream)), "moe_unpermute_combine")
+
+
+# ---------------------------------------------------------------- 16-bit weights
+def _ld(t):
+    """Row stride in elements of a [rows][cols] tensor whose rows are contiguous.  A single row has no next
+    one: any stride that the call accepts will do."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise MoeError(MOE_ERR_INVALID_ARG, "row elements must be contiguous")
+    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _here(*tensors):
+    """The tensors live on the current CUDA device, the one whose stream the call is enqueued on."""
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2  # -1: a CPU tensor
+    if any(t is not None and t.get_device() != dev for t in tensors):
+        raise MoeError(MOE_ERR_INVALID_ARG, "tensors must be on the current CUDA device")
+
+
+def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False, stream=None):
+    """y [T][N] = act(x w^T + bias) + residual, or with gated (w [2N][K], gate rows first) act(g) * u + residual.
+    x [T][K], w, bias and residual are bf16 (or int16 bits) or f16; y is of the same type or fp32.  Tensors may
+    be rows of wider buffers (row strides of x and w in multiples of 8 elements)."""
+    import torch
+    T, K = x.shape
+    N = y.shape[1]
+    if (w.shape != ((2 * N if gated else N), K) or y.shape[0] != T
+            or (bias is not None and (bias.numel() != w.shape[0] or not bias.is_contiguous()))
+            or (residual is not None and residual.shape != y.shape)
+            or any(t is not None and t.dtype != x.dtype for t in (w, bias, residual))
+            or y.dtype not in (x.dtype, torch.float32) or x.element_size() != 2):
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_linear")
+    _here(x, w, y, bias, residual)
+    dt = MOE_F16 if x.dtype == torch.float16 else MOE_BF16
+    _check(lib().moe_linear(x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), T, N, K, dt, _p(bias), act, int(gated),
+                            _p(residual), 0 if residual is None else _ld(residual), y.data_ptr(), _ld(y),
+                            MOE_F32 if y.dtype == torch.float32 else dt, _stream(stream)), "moe_linear")
+
+
+def make_bf16_layer(E, H, F, gate_up, down) -> moe_bf16_layer:
+    """Host descriptor of one layer's bf16 experts: gate_up [E][2F][H], down [E][H][F] (device buffers)."""
+    return moe_bf16_layer(E, H, F, gate_up.data_ptr(), down.data_ptr())
+
+
+def moe_decode_layer_bf16_workspace_bytes(T, k, shared, E, H, F) -> int:
+    return lib().moe_decode_layer_bf16_workspace_bytes(T, k, shared, E, H, F)
+
+
+def moe_decode_layer_bf16(layer: moe_bf16_layer, x, k, y, ws, wr=None, logits=None, shared=0, shared_gate=None,
+                          residual=None, idx=None, w=None, stream=None):
+    """One layer with bf16 experts: the router (from wr, or logits as given), routing, expert FFN, the optional
+    shared expert (with its sigmoid gate), combine, residual."""
+    _here(x, wr, logits, y, ws, shared_gate, residual, idx, w)
+    T = x.shape[0]
+    _check(lib().moe_decode_layer_bf16(ctypes.byref(layer), _p(x), _p(wr), _p(logits), T, k, shared, _p(shared_gate),
+                                       _p(residual), _p(y), _p(idx), _p(w), _p(ws), ws.numel() * ws.element_size(),
+                                       _stream(stream)), "moe_decode_layer_bf16")
+
+
+def moe_prefill_bf16_workspace_bytes(rows, F) -> int:
+    return lib().moe_prefill_bf16_workspace_bytes(rows, F)
+
+
+def moe_ffn_grouped_prefill_bf16(layer: moe_bf16_layer, x_perm, offsets, y_perm, ws, stream=None):
+    _here(x_perm, offsets, y_perm, ws)
+    rows = x_perm.shape[0]
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().moe_ffn_grouped_prefill_bf16(ctypes.byref(layer), _p(x_perm), _p(offsets), rows, _p(y_perm), _p(ws),
+                                              nbytes, _stream(stream)), "moe_ffn_grouped_prefill_bf16")
 
 
 def moe_device_error(stream=None) -> int:

@@ -1,0 +1,255 @@
+"""GPU parity of moe_linear against the definition in 64 bits.
+
+Small integers make every product and partial sum an exact fp32 value whatever
+the order, so those tests ask for equality.  On random values the tolerance
+counts, per element:
+  - the fp32 sum: K products in any order, each addition off by at most one
+    unit in the last place: A = (K + 2) 2^-23 (sum |x||w| + |bias|);
+  - the activation: its slope (at most 1.2 for all of them) times A, and its own
+    evaluation, at most 2^-19 of the larger of its value and 2^-2 (the
+    error of exp at |argument| <= 32: 2 + 1.2 * 32 ulps of 2^-23);
+  - for gated products both factors' errors times the other factor;
+  - one fp32 rounding of each of the remaining steps (2^-22 of the values), and
+    the final rounding: eps / 2 of the value (plus half the smallest f16
+    subnormal, 2^-25).
+"""
+import pytest
+import torch
+
+import quantized_moe_route_b200 as moe
+
+pytestmark = pytest.mark.gpu
+
+ACTS = {"none": lambda v: v, "silu": lambda v: v * torch.special.expit(v),
+        "gelu": lambda v: v * torch.special.ndtr(v),
+        "gelu_tanh": lambda v: 0.5 * v * (1 + torch.tanh((2 / torch.pi) ** 0.5 * (v + 0.044715 * v ** 3))),
+        "relu": lambda v: v.clamp(min=0), "sigmoid": torch.special.expit}
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def act_id(name):
+    return getattr(moe, "MOE_ACT_" + name.upper())
+
+
+def padded(rows, cols, ld, dtype, fill=float("nan")):
+    """A [rows][cols] view of a wider buffer whose tails hold `fill`."""
+    buf = torch.full((rows, ld), fill, dtype=dtype, device="cuda")
+    return buf, buf[:, :cols]
+
+
+def ints(gen, shape, dtype, lim=3):
+    return torch.randint(-lim, lim + 1, shape, generator=gen, device="cuda").to(dtype)
+
+
+def up8(k):
+    return (k + 7) // 8 * 8
+
+
+# T around the tile and token-group edges, N and K odd, tiny, and past the tiles
+EXACT = [(1, 1, 1), (1, 16, 8), (1, 2048, 2048), (2, 5, 7), (3, 100, 40), (4, 17, 72), (7, 512, 2048), (8, 129, 100),
+         (9, 1000, 512), (13, 4099, 1000), (15, 300, 264), (16, 2048, 2048), (16, 33, 4104), (5, 24, 16384),
+         (1, 7, 40000), (17, 128, 64), (17, 127, 2050), (31, 257, 33), (33, 2049, 96), (64, 512, 2048), (100, 96, 8200),
+         (127, 640, 129), (128, 128, 128), (129, 2048, 512), (200, 130, 65), (255, 1, 1000), (256, 256, 256),
+         (257, 385, 640), (300, 5, 15), (513, 1025, 320), (1000, 264, 192), (2050, 384, 72)]
+
+
+@pytest.mark.parametrize("T,N,K", EXACT)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_integers_are_exact(T, N, K, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(T * 131 + N * 17 + K)
+    dt = DT[dtype]
+    _, x = padded(T, K, up8(K) + 8 * (T % 3), dt)
+    _, w = padded(N, K, up8(K) + 8 * (N % 2), dt)
+    x.copy_(ints(gen, (T, K), dt))
+    w.copy_(ints(gen, (N, K), dt))
+    bias = ints(gen, (N,), dt, 50)
+    ybuf, y = padded(T, N, N + 5, torch.float32, 777.0)
+    moe.moe_linear(x, w, y, bias=bias)
+    want = x.double() @ w.double().t() + bias.double()
+    assert torch.equal(y.double(), want)
+    assert (ybuf[:, N:] == 777.0).all(), "wrote past the row"
+    # 16-bit output: the exact value rounded once, on a residual that y replaces
+    rbuf, r = padded(T, N, N + 3, dt, 5.0)
+    r.copy_(ints(gen, (T, N), dt, 100))
+    want16 = (want + r.double()).float().to(dt)
+    moe.moe_linear(x, w, r, bias=bias, residual=r)
+    assert torch.equal(r, want16)
+    assert (rbuf[:, N:] == 5.0).all()
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 512, 2048), (3, 13, 24), (9, 65, 136), (16, 1000, 520), (40, 64, 72), (130, 200, 300),
+                                   (300, 512, 2048), (700, 129, 65)])
+def test_gated_integers_are_exact(T, N, K):
+    gen = torch.Generator(device="cuda").manual_seed(T + N + K)
+    dt = torch.float16
+    _, x = padded(T, K, up8(K), dt)
+    x.copy_(ints(gen, (T, K), dt, 2))
+    w = torch.zeros((2 * N, up8(K)), dtype=dt, device="cuda")[:, :K]
+    w.copy_(ints(gen, (2 * N, K), dt, 2))
+    bias = ints(gen, (2 * N,), dt)
+    y = torch.empty((T, N), dtype=torch.float32, device="cuda")
+    moe.moe_linear(x, w, y, bias=bias, act=moe.MOE_ACT_RELU, gated=True)
+    v = x.double() @ w.double().t() + bias.double()
+    want = v[:, :N].clamp(min=0) * v[:, N:]
+    assert want.abs().max() < 2 ** 24
+    assert torch.equal(y.double(), want)
+
+
+def check_random(T, N, K, dtype, act, gated, bias, residual, out32, pad, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    dt, rows = DT[dtype], 2 * N if gated else N
+    _, x = padded(T, K, up8(K) + pad, dt)
+    _, w = padded(rows, K, up8(K) + pad, dt)
+    x.copy_(torch.randn((T, K), generator=gen, device="cuda"))
+    w.copy_(torch.randn((rows, K), generator=gen, device="cuda") * K ** -0.5)
+    b = (0.5 * torch.randn(rows, generator=gen, device="cuda")).to(dt) if bias else None
+    r = torch.randn((T, N + pad), generator=gen, device="cuda").to(dt)[:, :N] if residual else None
+    ybuf, y = padded(T, N, N + pad + 1, torch.float32 if out32 else dt, 3.0)
+    moe.moe_linear(x, w, y, bias=b, residual=r, act=act_id(act), gated=gated)
+    xd, wd = x.double(), w.double()
+    bd = b.double() if bias else torch.zeros(rows, dtype=torch.float64, device="cuda")
+    v = xd @ wd.t() + bd
+    A = (K + 2) * 2.0 ** -23 * (xd.abs() @ wd.abs().t() + bd.abs())
+    a = ACTS[act](v[:, :N])
+    Ea = 1.2 * A[:, :N] + (0 if act in ("none", "relu") else 2.0 ** -19 * a.abs().clamp(min=0.25))
+    if gated:
+        u = v[:, N:]
+        want = a * u
+        tol = Ea * (u.abs() + A[:, N:]) + a.abs() * A[:, N:] + 2.0 ** -22 * want.abs()
+    else:
+        want, tol = a, Ea
+    if residual:
+        want = want + r.double()
+        tol = tol + 2.0 ** -22 * (want.abs() + r.double().abs())
+    if not out32:
+        tol = tol + torch.finfo(dt).eps / 2 * (want.abs() + tol) + 2.0 ** -25
+    err = (y.double() - want).abs()
+    assert (err <= tol).all(), f"worst {((err - tol).max()):.3e} past the bound"
+    # the same on the whole: rounding to the output type, and the fp32 sums
+    # (2^-20 of the values, far above sqrt(K) 2^-24)
+    rel = (err.norm() / want.norm()).item()
+    assert rel <= (2.0 ** -20 if out32 else torch.finfo(dt).eps / 2), rel
+    assert (ybuf[:, N:] == 3.0).all()
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T,N,K,dtype,out32", [(1, 512, 2048, "bf16", False), (6, 77, 136, "f16", True),
+                                               (16, 300, 1000, "bf16", True), (90, 200, 264, "f16", False),
+                                               (300, 513, 2048, "bf16", False)])
+def test_random_values(T, N, K, dtype, out32, act, gated):
+    check_random(T, N, K, dtype, act, gated, True, True, out32, 8, T + N)
+
+
+@pytest.mark.parametrize("bias,residual", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("T", [1, 12, 60, 400])
+def test_optional_terms(T, bias, residual):
+    check_random(T, 384, 512, "bf16", "silu", False, bias, residual, False, 0, T)
+    check_random(T, 200, 512, "f16", "gelu", True, bias, residual, True, 16, T + 1)
+
+
+def test_same_bits_every_call_and_on_another_stream():
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for T, N, K in [(3, 512, 2048), (48, 256, 4096), (400, 1000, 512)]:
+        x = torch.randn((T, K), generator=gen, device="cuda").bfloat16()
+        w = torch.randn((N, K), generator=gen, device="cuda").bfloat16()
+        ys = [torch.empty((T, N), device="cuda") for _ in range(4)]
+        moe.moe_linear(x, w, ys[0])
+        moe.moe_linear(x, w, ys[1])
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        moe.moe_linear(x, w, ys[2], stream=s)
+        with torch.cuda.stream(s):
+            moe.moe_linear(x, w, ys[3])
+        torch.cuda.synchronize()
+        assert all(torch.equal(ys[0], y) for y in ys[1:])
+
+
+def test_two_calls_at_once_on_two_streams():
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = [ints(gen, (40, 2048), torch.bfloat16) for _ in range(2)]
+    w = [ints(gen, (2048, 2048), torch.bfloat16) for _ in range(2)]
+    y = [torch.empty((40, 2048), device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(2):
+            moe.moe_linear(x[i], w[i], y[i], stream=streams[i])
+            moe.moe_linear(x[i][:3], w[i], y[i][:3], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(y[i].double(), x[i].double() @ w[i].double().t())
+
+
+def test_captured_chain_replays_on_new_inputs():
+    """A shared expert as two linears in one graph: gated up, then down onto the residual stream in place."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    T, H, F = 5, 512, 256
+    x, wu, wd = ints(gen, (T, H), torch.bfloat16, 1), ints(gen, (2 * F, H), torch.bfloat16, 1), ints(
+        gen, (H, F), torch.bfloat16, 1)
+    h, r = torch.empty((T, F), dtype=torch.bfloat16, device="cuda"), torch.empty((T, H), device="cuda").bfloat16()
+    y = torch.empty((T, H), device="cuda")
+
+    def chain():
+        moe.moe_linear(x, wu, h, act=moe.MOE_ACT_RELU, gated=True)
+        moe.moe_linear(h, wd, y, residual=r)
+
+    chain()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain()
+    for seed in range(3):
+        x.copy_(ints(gen, (T, H), torch.bfloat16, 1))
+        r.copy_(ints(gen, (T, H), torch.bfloat16, 9))
+        g.replay()
+        torch.cuda.synchronize()
+        v = x.double() @ wu.double().t()
+        hh = (v[:, :F].clamp(min=0) * v[:, F:]).float().bfloat16()
+        # |h| < 2^8 * 2^7 holds 8 bits each; sums of F values of at most 2^15 in steps of 2^0 stay exact below 2^24
+        assert torch.equal(h, hh)
+        assert torch.equal(y.double(), hh.double() @ wd.double().t() + r.double())
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_offsets_past_32_bits(T):
+    """Rows of w, x, y and residual so far apart that element offsets pass 2^31."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    N, K, far = 40, 72, (1 << 31) // 32 + 8
+    w = torch.empty(far * (N - 1) + K, dtype=torch.bfloat16, device="cuda").as_strided((N, K), (far, 1))
+    xs = (1 << 31) // (T - 1) + 8
+    xs += -xs % 8
+    x = torch.empty(xs * (T - 1) + K, dtype=torch.bfloat16, device="cuda").as_strided((T, K), (xs, 1))
+    y = torch.empty(xs * (T - 1) + N, dtype=torch.bfloat16, device="cuda").as_strided((T, N), (xs, 1))
+    w.copy_(ints(gen, (N, K), torch.bfloat16))
+    x.copy_(ints(gen, (T, K), torch.bfloat16))
+    y.copy_(ints(gen, (T, N), torch.bfloat16))
+    want = (x.double() @ w.double().t() + y.double()).float().bfloat16()
+    moe.moe_linear(x, w, y, residual=y)
+    assert torch.equal(y, want)
+
+
+def test_infinite_and_large_values_keep_their_meaning():
+    """Values past the f16 range round to infinity; silu and sigmoid reach their limits at +-large."""
+    K = 64
+    x = torch.ones((3, K), dtype=torch.float16, device="cuda")
+    x[1] = -1
+    x[2] = 0
+    w = torch.full((20, K), 1200.0, dtype=torch.float16, device="cuda")
+    y = torch.empty((3, 20), dtype=torch.float16, device="cuda")
+    moe.moe_linear(x, w, y)
+    assert torch.isposinf(y[0]).all() and torch.isneginf(y[1]).all() and (y[2] == 0).all()
+    for act, lims in (("silu", (float("inf"), 0.0, 0.0)), ("sigmoid", (1.0, 0.0, 0.5)), ("gelu", (float("inf"), 0.0, 0.0)),
+                      ("gelu_tanh", (float("inf"), 0.0, 0.0)), ("relu", (float("inf"), 0.0, 0.0))):
+        moe.moe_linear(x, w, y, act=act_id(act))
+        for t in range(3):
+            assert (y[t] == lims[t]).all(), act
+
+
+def test_empty_calls_write_nothing():
+    x, w = torch.ones((4, 16), device="cuda").bfloat16(), torch.ones((8, 16), device="cuda").bfloat16()
+    y = torch.full((4, 8), 9.0, device="cuda")
+    moe.moe_linear(x[:0], w, y[:0])
+    moe.moe_linear(x, w[:0], y[:, :0])
+    torch.cuda.synchronize()
+    assert (y == 9.0).all()

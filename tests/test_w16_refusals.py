@@ -1,0 +1,118 @@
+"""Refusals and no-ops of the 16-bit-weight calls.  Argument errors are found
+on the host before any launch, so all of this runs without a GPU (the
+pointers are never followed)."""
+import ctypes
+
+import pytest
+import torch
+
+import quantized_moe_route_b200 as moe
+
+INV, SHAPE, WS = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED_SHAPE, moe.MOE_ERR_WORKSPACE
+P = 1 << 20  # an aligned address that is never followed
+
+
+def linear(x=P, ldx=64, w=P, ldw=64, T=4, N=32, K=64, dtype=moe.MOE_BF16, bias=None, act=0, gated=0, residual=None,
+           ldr=0, y=P, ldy=32, y_dtype=None):
+    y_dtype = dtype if y_dtype is None else y_dtype
+    return moe.lib().moe_linear(x, ldx, w, ldw, T, N, K, dtype, bias, act, gated, residual, ldr, y, ldy, y_dtype, None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INV, dict(T=-1)), (INV, dict(N=-1)), (INV, dict(K=0)), (INV, dict(K=-8)),
+    (INV, dict(dtype=moe.MOE_F32)), (INV, dict(dtype=3)), (INV, dict(y_dtype=moe.MOE_F16)),
+    (INV, dict(dtype=moe.MOE_F16, y_dtype=moe.MOE_BF16)), (INV, dict(act=-1)), (INV, dict(act=6)),
+    (INV, dict(gated=2)), (INV, dict(gated=-1)),
+    (INV, dict(x=None)), (INV, dict(w=None)), (INV, dict(y=None)),
+    (INV, dict(ldx=56)), (INV, dict(ldw=56)), (INV, dict(ldy=31)), (INV, dict(residual=P, ldr=31)),
+    (INV, dict(x=P + 8)), (INV, dict(w=P + 2)), (INV, dict(y=P + 1)), (INV, dict(y=P + 2, y_dtype=moe.MOE_F32)),
+    (INV, dict(bias=P + 1)), (INV, dict(residual=P + 1, ldr=32)),
+    (INV, dict(residual=P, ldr=40, ldy=32)), (INV, dict(residual=P, ldr=32, y_dtype=moe.MOE_F32)),
+    (SHAPE, dict(ldx=68)), (SHAPE, dict(ldw=65)), (SHAPE, dict(ldx=(1 << 38) + 8)),
+    (SHAPE, dict(N=(1 << 30) + 1, ldy=1 << 31)),
+    (moe.MOE_OK, dict(T=0)), (moe.MOE_OK, dict(N=0)), (moe.MOE_OK, dict(T=0, x=None, w=None, y=None)),
+])
+def test_linear_refusals(want, kw):
+    assert linear(**kw) == want
+
+
+def test_linear_binding_refuses_what_the_abi_cannot_see():
+    bf = torch.bfloat16
+    x, w, y = torch.zeros(2, 16, dtype=bf), torch.zeros(8, 16, dtype=bf), torch.zeros(2, 8, dtype=bf)
+    bad = [
+        dict(y=torch.zeros(3, 8, dtype=bf)), dict(y=torch.zeros(2, 4, dtype=bf)), dict(x=x.half()),
+        dict(y=y.half()), dict(bias=torch.zeros(8)), dict(bias=torch.zeros(7, dtype=bf)),
+        dict(bias=torch.zeros(16, dtype=bf)[::2]), dict(residual=torch.zeros(2, 7, dtype=bf)), dict(gated=True),
+        dict(x=torch.zeros(16, 2, dtype=bf).t()), dict(x=x.float(), w=w.float()),
+        {},  # CPU tensors
+    ]
+    for kw in bad:
+        a = dict(x=x, w=w, y=y)
+        a.update(kw)
+        with pytest.raises(moe.MoeError) as ei:
+            moe.moe_linear(**a)
+        assert ei.value.status == INV, kw
+
+
+def decode(E=8, H=128, F=64, gu=P, dn=P, x=P, wr=P, logits=None, T=2, k=2, shared=0, sg=None, residual=None, y=P,
+           idx=None, w=None, ws=P, ws_bytes=1 << 40):
+    layer = moe.moe_bf16_layer(E, H, F, gu, dn)
+    return moe.lib().moe_decode_layer_bf16(ctypes.byref(layer), x, wr, logits, T, k, shared, sg, residual, y, idx, w,
+                                           ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INV, dict(T=-1)), (INV, dict(k=0)), (INV, dict(shared=2)), (INV, dict(shared=-1)), (INV, dict(E=0)),
+    (INV, dict(H=0)), (INV, dict(F=-64)), (INV, dict(k=9)), (INV, dict(k=8, shared=1)), (INV, dict(E=1, k=1, shared=1)),
+    (INV, dict(sg=P)), (INV, dict(gu=None)), (INV, dict(dn=None)), (INV, dict(x=None)), (INV, dict(y=None)),
+    (INV, dict(wr=None)), (INV, dict(idx=P)), (INV, dict(w=P)),
+    (INV, dict(gu=P + 8)), (INV, dict(dn=P + 8)), (INV, dict(x=P + 2)), (INV, dict(wr=P + 2)), (INV, dict(y=P + 4)),
+    (INV, dict(residual=P + 2)), (INV, dict(shared=1, sg=P + 2)), (INV, dict(ws=P + 8)), (INV, dict(logits=P + 2)),
+    (INV, dict(idx=P + 2, w=P)), (INV, dict(idx=P, w=P + 1)),
+    (SHAPE, dict(H=96)), (SHAPE, dict(F=32)), (SHAPE, dict(T=17)), (SHAPE, dict(E=64, T=16, k=17)),
+    (SHAPE, dict(E=1025)), (SHAPE, dict(E=64, T=1, k=33)), (SHAPE, dict(E=64, T=1, k=32, shared=1)),
+    (SHAPE, dict(E=64, T=16, k=16, shared=1)),
+    (WS, dict(ws=None)), (WS, dict(ws_bytes=100)), (moe.MOE_OK, dict(T=0)),
+])
+def test_decode_layer_refusals(want, kw):
+    assert decode(**kw) == want
+
+
+def test_decode_layer_null_struct_and_workspace_size():
+    L = moe.lib()
+    assert L.moe_decode_layer_bf16(None, P, P, None, 1, 1, 0, None, None, P, None, None, P, 1 << 30, None) == INV
+    need = moe.moe_decode_layer_bf16_workspace_bytes(2, 2, 0, 8, 128, 64)
+    assert need > 0 and decode(ws_bytes=need - 1) == WS
+    for bad in [(0, 2, 0, 8, 128, 64), (2, 0, 0, 8, 128, 64), (2, 2, 2, 8, 128, 64), (2, 2, 0, 0, 128, 64),
+                (2, 2, 1, 1, 128, 64), (2, 2, 0, 8, 0, 64), (2, 2, 0, 8, 128, 0)]:
+        assert moe.moe_decode_layer_bf16_workspace_bytes(*bad) == 0
+
+
+def grouped(E=8, H=128, F=64, gu=P, dn=P, x=P, offsets=P, rows=4, y=P, ws=P, ws_bytes=1 << 40):
+    layer = moe.moe_bf16_layer(E, H, F, gu, dn)
+    return moe.lib().moe_ffn_grouped_prefill_bf16(ctypes.byref(layer), x, offsets, rows, y, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INV, dict(rows=-1)), (INV, dict(E=0)), (INV, dict(H=0)), (INV, dict(F=0)), (INV, dict(gu=None)),
+    (INV, dict(dn=None)), (INV, dict(x=None)), (INV, dict(offsets=None)), (INV, dict(y=None)),
+    (INV, dict(x=P + 8)), (INV, dict(y=P + 8)), (INV, dict(gu=P + 2)), (INV, dict(dn=P + 2)), (INV, dict(ws=P + 8)),
+    (INV, dict(offsets=P + 2)),
+    (SHAPE, dict(H=32)), (SHAPE, dict(F=96)), (SHAPE, dict(E=1025)),
+    (WS, dict(ws=None)), (WS, dict(ws_bytes=4 * 64 * 2 - 1)), (moe.MOE_OK, dict(rows=0)),
+    (moe.MOE_OK, dict(rows=0, gu=None, dn=None, x=None, offsets=None, y=None, ws=None)),
+])
+def test_grouped_refusals(want, kw):
+    assert grouped(**kw) == want
+
+
+def test_bf16_bindings_refuse_cpu_tensors():
+    bf = torch.bfloat16
+    layer = moe.moe_bf16_layer(8, 128, 64, P, P)
+    x, y, ws = torch.zeros(2, 128, dtype=bf), torch.zeros(2, 128, dtype=bf), torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(moe.MoeError) as ei:
+        moe.moe_decode_layer_bf16(layer, x, 2, y, ws, logits=torch.zeros(2, 8))
+    assert ei.value.status == INV
+    with pytest.raises(moe.MoeError) as ei:
+        moe.moe_ffn_grouped_prefill_bf16(layer, x, torch.zeros(9, dtype=torch.int32), y, ws)
+    assert ei.value.status == INV
