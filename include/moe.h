@@ -574,7 +574,7 @@ typedef enum {
  * y may be the residual itself (same address, type and row stride); beyond
  * that no output may overlap an input.
  * Requirements: x and w 16-byte aligned, ldx % 8 == 0 and ldw % 8 == 0, N <=
- * 2^30, row strides below 2^38; any T, N, K.  T == 0 or N == 0 is a no-op.
+ * 2^29, row strides up to 2^38; any T, N, K.  T == 0 or N == 0 is a no-op.
  * No workspace.  Errors: INVALID_ARG (null, a negative size, K == 0, an unknown type
  * or activation, a row stride below its row's length, misalignment),
  * UNSUPPORTED_SHAPE, CUDA.

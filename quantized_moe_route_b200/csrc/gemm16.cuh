@@ -1,0 +1,431 @@
+// gemm16.cuh -- the tensor-core product behind moe_linear and the grouped
+// FFN with bf16 experts: y = epilogue(x W^T) for 16-bit x [rows][K] and W
+// [outputs][K], both K-major as they lie in memory, dense or with the rows
+// of x grouped by expert.
+//
+// The weights are the MMA's A operand (M = 128 outputs), the rows of x its N
+// (up to kNT, trimmed to the valid rows rounded up to 16), so one kernel fits
+// any number of rows and a lane of tensor memory is an output: bias is one
+// value a lane, and a warp's store is 32 consecutive outputs of one row.  A
+// tile is a chunk of rows of one expert and kMats blocks of 128 outputs that
+// share the chunk's operand: gate and up of 128 features, or 256 consecutive
+// outputs, or (kMats = 1, kNT = 256) 128 outputs.
+//
+// Warp 0 loads 64-channel stages by TMA (128-byte swizzle; out-of-range rows
+// and channels arrive as zeros), warp 1 issues tcgen05.mma into one of two
+// accumulator sets in tensor memory, warps 2-9 run the epilogue of the other
+// set.  Products with too few tiles for the GPU split K over a cluster of
+// CTAs instead of looping over tiles: each leaves its fp32 partial in shared
+// memory, and CTA r adds up the rows r, r + S, ... in rank order through
+// distributed shared memory (a fixed order: the same bits every call).
+#pragma once
+#include "tcgen05.cuh"
+#include "w16.cuh"
+
+namespace moe {
+
+constexpr int kG16BK = 64;
+constexpr int kG16Stages = 4;
+constexpr int kG16EpiWarps = 8;
+constexpr int kG16Threads = (2 + kG16EpiWarps) * 32;
+constexpr uint32_t kG16WaitPolls = 1u << 18;  // sleeping polls of up to 10 us: a bound of seconds
+
+struct Gemm16Args {
+  const int32_t *offsets;  // grouped: [E + 1]; dense: NULL
+  int E;                   // grouped: experts; dense: 1
+  int rows, N, K;          // N: outputs (features when gated)
+  int w_rows;              // weight rows per expert
+  int mat_off;             // weight rows from a tile's block 0 to its block 1
+  int nfb;                 // output blocks per row chunk
+  int nt;                  // rows per chunk (at most kNT, a multiple of 16)
+  int splits;              // CTAs of a cluster that share a tile (1: none, persistent over tiles)
+  const uint16_t *bias, *residual;
+  void *y;
+  int64_t ldr, ldy;
+  int act, y_f32;
+  int *err;
+};
+
+template <int kMats, int kNT>
+struct Gemm16Cfg {
+  static constexpr uint32_t kABytes = kMats * 128 * 128;  // 128 rows of 64 channels per block
+  static constexpr uint32_t kBBytes = kNT * 128;
+  static constexpr uint32_t kStage = kABytes + kBBytes;
+  static constexpr uint32_t kTailOff = kG16Stages * kStage;
+  static constexpr uint32_t kTableInts = 1024 + 1;
+  static constexpr uint32_t kSmemBytes = kTailOff + 1024 /* alignment */ + 256 + kTableInts * 4;
+  static constexpr uint32_t kAccCols = kMats * kNT;
+  static_assert(2 * kAccCols <= 512, "two accumulator sets in tensor memory");
+  static_assert(kMats * 128 * kNT * 4 <= kTailOff, "split partials fit in the ring");
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+struct Gemm16Tile {
+  int row0, nvalid, n0, wrow;  // rows of x, first output, first weight row
+};
+
+// Tile t: chunk t / nfb, output block t % nfb.  start[e]: first chunk of expert e.
+template <bool kGrouped, int kOut>
+__device__ __forceinline__ Gemm16Tile gemm16_tile(const Gemm16Args &a, const int *start, int t) {
+  Gemm16Tile ti;
+  const int chunk = t / a.nfb;
+  ti.n0 = (t - chunk * a.nfb) * kOut;
+  if (kGrouped) {
+    const int e = last_at_or_below(start, a.E, chunk);
+    const int o0 = clamped_offset(a.offsets, e, a.rows), o1 = clamped_offset(a.offsets, e + 1, a.rows);
+    ti.row0 = o0 + (chunk - start[e]) * a.nt;
+    ti.nvalid = min(a.nt, o1 - ti.row0);
+    ti.wrow = e * a.w_rows + ti.n0;
+  } else {
+    ti.row0 = chunk * a.nt;
+    ti.nvalid = min(a.nt, a.rows - ti.row0);
+    ti.wrow = ti.n0;
+  }
+  return ti;
+}
+
+template <int kN>
+__device__ __forceinline__ void activate_all(float (&v)[kN], int act) {
+  switch (act) {  // the branch is uniform: one loop each
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_SILU);
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_GELU);
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_GELU_TANH);
+      break;
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_RELU);
+      break;
+    case MOE_ACT_SIGMOID:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_SIGMOID);
+      break;
+    default: break;
+  }
+}
+
+// kN rows (row0 + i * step, the first nv of them valid) of output n from
+// their products p0 (and, gated, p1): bias, activation, gate, residual, store.
+template <bool kGated, bool kF16, int kN>
+__device__ __forceinline__ void gemm16_emit(const Gemm16Args &a, int n, int64_t row0, int step, int nv, float (&p0)[kN],
+                                            float (&p1)[kN]) {
+  if (n >= a.N) return;
+  float r[kN];
+  const uint16_t *rp = a.residual + row0 * a.ldr + n;
+  if (a.residual) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) r[i] = i < nv ? w16_to_f32<kF16>(rp[i * step * a.ldr]) : 0.f;
+  }
+  if (a.bias) {
+    const float b0 = w16_to_f32<kF16>(a.bias[n]);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) p0[i] += b0;
+  }
+  activate_all(p0, a.act);
+  if (kGated) {
+    const float b1 = a.bias ? w16_to_f32<kF16>(a.bias[a.N + n]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) p0[i] *= p1[i] + b1;
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) p0[i] += r[i];
+  }
+  const int64_t o = row0 * a.ldy + n, dy = step * a.ldy;
+  if (a.y_f32) {
+    float *y = static_cast<float *>(a.y) + o;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < nv) y[i * dy] = p0[i];
+  } else {
+    uint16_t *y = static_cast<uint16_t *>(a.y) + o;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < nv) y[i * dy] = f32_to_w16<kF16>(p0[i]);
+  }
+}
+
+template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16>
+__global__ void __launch_bounds__(kG16Threads, 1)
+    gemm16_kernel(Gemm16Args a, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x64_map,
+                  const __grid_constant__ CUtensorMap x16_map) {
+  using C = Gemm16Cfg<kMats, kNT>;
+  static_assert(!kGated || kMats == 2, "gate and up");
+  constexpr int kOut = kGated ? 128 : 128 * kMats;  // outputs per tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kTailOff);
+  uint64_t *empty = full + kG16Stages;
+  uint64_t *acc_full = empty + kG16Stages;  // [2]
+  uint64_t *acc_empty = acc_full + 2;       // [2]
+  uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(acc_empty + 2);
+  volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
+  int *start = reinterpret_cast<int *>(smem + C::kTailOff + 256);  // [E + 1]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kG16Stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kG16EpiWarps * 32);
+    }
+    *abort_s = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_base_s, 2 * C::kAccCols);
+  grid_dep_wait();
+  if (kGrouped && warp == 2) {  // chunk table: exclusive scan of the experts' chunk counts
+    int carry = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < a.E ? max(clamped_offset(a.offsets, e + 1, a.rows) - clamped_offset(a.offsets, e, a.rows), 0) : 0;
+      const int c = (n + a.nt - 1) / a.nt;
+      int v = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      if (e < a.E) start[e] = carry + v - c;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) start[a.E] = carry;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_trigger();
+  const uint32_t tmem = *tmem_base_s;
+  const int nchunks = kGrouped ? start[a.E] : (a.rows + a.nt - 1) / a.nt;
+  const int ntiles = nchunks * a.nfb;
+  const int S = a.splits, rank = S > 1 ? (int)cluster_rank() : 0;
+  const int t0 = blockIdx.x / S, G = gridDim.x / S;
+  const int KB = (a.K + kG16BK - 1) / kG16BK;
+  const int kb0 = KB * rank / S, kb1 = KB * (rank + 1) / S;  // S <= KB: never empty
+  auto fail = [&]() {
+    atomicExch(a.err, DEVERR_PREFILL_WAIT);
+    *abort_s = 1;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (int t = t0; t < ntiles && !*abort_s; t += G) {
+        const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
+        const int nrows = (ti.nvalid + 15) & ~15;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % kG16Stages;
+          if (!mbar_wait_sleep(&empty[s], ((it / kG16Stages) & 1u) ^ 1u, kG16WaitPolls)) {
+            fail();
+            break;
+          }
+          uint8_t *at = smem + s * C::kStage, *bt = at + C::kABytes;
+          mbar_arrive_expect_tx(&full[s], C::kABytes + (uint32_t)nrows * 128u);
+#pragma unroll
+          for (int m = 0; m < kMats; ++m)
+            tma_load_2d(at + m * 128 * 128, &w_map, kb * kG16BK, ti.wrow + m * a.mat_off, &full[s]);
+          int r = 0;  // boxes of 64 rows, then of 16
+          for (; r + 64 <= nrows; r += 64) tma_load_2d(bt + r * 128, &x64_map, kb * kG16BK, ti.row0 + r, &full[s]);
+          for (; r < nrows; r += 16) tma_load_2d(bt + r * 128, &x16_map, kb * kG16BK, ti.row0 + r, &full[s]);
+        }
+      }
+      // the last load issued into each stage lands before the CTA leaves
+      if (*abort_s)
+        for (uint32_t j = it > kG16Stages ? it - kG16Stages : 0u; j < it; ++j)
+          mbar_wait_sleep(&full[j % kG16Stages], (j / kG16Stages) & 1u, kG16WaitPolls);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+      uint32_t it = 0, tc = 0;
+      for (int t = t0; t < ntiles && !*abort_s; t += G, ++tc) {
+        const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
+        const uint32_t idesc = idesc_16_f32((ti.nvalid + 15) & ~15, kF16);
+        const uint32_t acc = tmem + (tc & 1u) * C::kAccCols;
+        if (!mbar_wait_sleep(&acc_empty[tc & 1u], ((tc >> 1) & 1u) ^ 1u, kG16WaitPolls)) {
+          fail();
+          break;
+        }
+        tc_fence_after();
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % kG16Stages;
+          if (!mbar_wait_sleep(&full[s], (it / kG16Stages) & 1u, kG16WaitPolls)) {
+            fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = desc0 + ((uint32_t)s * C::kStage >> 4), bd = ad + (C::kABytes >> 4);
+#pragma unroll
+          for (int m = 0; m < kMats; ++m)
+#pragma unroll
+            for (int kk = 0; kk < kG16BK / 16; ++kk)
+              tc_mma_bf16(acc + m * kNT, ad + ((m * 128 * 128 + kk * 32) >> 4), bd + (kk * 32 >> 4), idesc,
+                          (kb > kb0 || kk) ? 1u : 0u);
+          tc_commit(&empty[s]);
+        }
+        if (!ok) break;
+        tc_commit(&acc_full[tc & 1u]);
+      }
+    }
+  } else {
+    // epilogue warps: lane quarter q holds outputs 32 q + lane of each block;
+    // the quarter's two warps take alternate groups of 16 rows
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint32_t tc = 0;
+    for (int t = t0; t < ntiles && !*abort_s; t += G, ++tc) {
+      const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
+      if (!mbar_wait_sleep(&acc_full[tc & 1u], (tc >> 1) & 1u, kG16WaitPolls)) {
+        fail();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc = tmem + (tc & 1u) * C::kAccCols + ((uint32_t)(q * 32) << 16);
+      const int n = ti.n0 + q * 32 + lane;
+      for (int c0 = half * 16; c0 < ti.nvalid; c0 += 32) {
+        uint32_t v[kMats][16];
+#pragma unroll
+        for (int m = 0; m < kMats; ++m) tmem_ld16_async(acc + m * kNT + c0, v[m]);
+        tmem_ld_wait();
+        float p[2][16];
+#pragma unroll
+        for (int m = 0; m < kMats; ++m) {
+          tmem_regs_after_wait(v[m]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) p[m][i] = __uint_as_float(v[m][i]);
+        }
+        if (S > 1) {  // partials: [block][row][128 outputs]
+          float *part = reinterpret_cast<float *>(smem);
+#pragma unroll
+          for (int m = 0; m < kMats; ++m)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) part[(m * kNT + c0 + i) * 128 + q * 32 + lane] = p[m][i];
+        } else {
+          gemm16_emit<kGated, kF16>(a, n, ti.row0 + c0, 1, ti.nvalid - c0, p[0], p[kMats - 1]);
+          if (kMats == 2 && !kGated)
+            gemm16_emit<false, kF16>(a, n + 128, ti.row0 + c0, 1, ti.nvalid - c0, p[1], p[1]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&acc_empty[tc & 1u]);
+    }
+  }
+  if (S > 1) {  // one tile per cluster; every thread of every CTA comes here, aborted or not
+    __syncwarp();
+    cluster_sync_all();
+    if (warp >= 2 && t0 < ntiles) {
+      const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t0);
+      const int q = warp & 3, half = (warp - 2) >> 2;
+      const int n = ti.n0 + q * 32 + lane;
+      const uint32_t part = smem_u32(smem) + (uint32_t)(q * 32 + lane) * 4u;
+      for (int c = rank + half * S; c < ti.nvalid; c += 2 * S) {
+        float p[2][1] = {};
+#pragma unroll
+        for (int m = 0; m < kMats; ++m)
+          for (int r = 0; r < S; ++r) p[m][0] += ld_dsmem_f32(part + (uint32_t)(m * kNT + c) * 512u, r);
+        gemm16_emit<kGated, kF16>(a, n, ti.row0 + c, 1, 1, p[0], p[kMats - 1]);
+        if (kMats == 2 && !kGated) gemm16_emit<false, kF16>(a, n + 128, ti.row0 + c, 1, 1, p[1], p[1]);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another may read its partials
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 2 * C::kAccCols);
+}
+
+// ---------------------------------------------------------------- host side
+// 16-bit [rows][cols] with a row stride of ld elements, boxes of 64 columns x
+// box_rows rows, 128-byte swizzle, zeros outside.
+inline bool gemm16_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f16) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct DeviceInfo {
+  int dev, sms;
+};
+// The current device and its SM count (looked up once per device).
+inline bool device_info(DeviceInfo *d) {
+  static std::atomic<int> sms[64];
+  cudaError_t e = cudaGetDevice(&d->dev);
+  if (e == cudaSuccess && (d->dev < 0 || d->dev >= 64)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess && (d->sms = sms[d->dev].load(std::memory_order_acquire)) == 0) {
+    e = cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->dev);
+    if (e == cudaSuccess) sms[d->dev].store(d->sms, std::memory_order_release);
+  }
+  if (e != cudaSuccess) set_cuda_error(e);
+  return e == cudaSuccess;
+}
+
+template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16>
+moe_status gemm16_launch(const Gemm16Args &a, int grid, const CUtensorMap &w, const CUtensorMap &x64,
+                         const CUtensorMap &x16, int dev, cudaStream_t stream) {
+  using C = Gemm16Cfg<kMats, kNT>;
+  auto kern = gemm16_kernel<kGrouped, kGated, kMats, kNT, kF16>;
+  static std::atomic<bool> attr_done[64];  // per device; the attribute call is idempotent
+  if (!attr_done[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
+    if (e != cudaSuccess) {
+      set_cuda_error(e);
+      return MOE_ERR_CUDA;
+    }
+    attr_done[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kG16Threads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, w, x64, x16);
+  if (e != cudaSuccess) {
+    set_cuda_error(e);
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // namespace moe

@@ -1,48 +1,31 @@
 // linear.cu -- y = act(x w^T + bias) + residual on 16-bit weights.
-//
-// One warp per output feature (and its gate) and four tokens: the lanes walk
-// the rows 32 elements at a time, fp32 FMAs, then a shuffle tree.
-#include "w16.cuh"
+#include "gemm16.cuh"
 
 namespace moe {
 
-struct LinearArgs {
-  const uint16_t *x, *w, *bias, *residual;
-  void *y;
-  int64_t ldx, ldw, ldr, ldy;
-  int T, N, K, act, gated, y_f32;
-};
-
-template <bool kF16>
-__global__ void __launch_bounds__(256) linear_kernel(LinearArgs a) {
-  grid_dep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t n = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (n >= a.N) return;
-  for (int64_t t0 = 4 * (int64_t)blockIdx.y; t0 < a.T; t0 += 4 * (int64_t)gridDim.y) {
-    float acc[2][4] = {};
-    for (int c = lane; c < a.K; c += 32) {
-      const float w0 = w16_to_f32<kF16>(a.w[n * a.ldw + c]);
-      const float w1 = a.gated ? w16_to_f32<kF16>(a.w[(n + a.N) * a.ldw + c]) : 0.f;
-      for (int i = 0; i < 4 && t0 + i < a.T; ++i) {
-        const float xv = w16_to_f32<kF16>(a.x[(t0 + i) * a.ldx + c]);
-        acc[0][i] = __fmaf_rn(xv, w0, acc[0][i]);
-        acc[1][i] = __fmaf_rn(xv, w1, acc[1][i]);
-      }
-    }
-    for (int i = 0; i < 4; ++i)
-      for (int m = 0; m < 2; ++m)
-        for (int o = 16; o > 0; o >>= 1) acc[m][i] += __shfl_xor_sync(0xffffffffu, acc[m][i], o);
-    for (int i = 0; i < 4 && t0 + i < a.T; ++i) {
-      if (lane != i) continue;
-      float v = acc[0][i] + (a.bias ? w16_to_f32<kF16>(a.bias[n]) : 0.f);
-      v = activate(v, a.act);
-      if (a.gated) v *= acc[1][i] + (a.bias ? w16_to_f32<kF16>(a.bias[n + a.N]) : 0.f);
-      if (a.residual) v += w16_to_f32<kF16>(a.residual[(t0 + i) * a.ldr + n]);
-      if (a.y_f32) static_cast<float *>(a.y)[(t0 + i) * a.ldy + n] = v;
-      else static_cast<uint16_t *>(a.y)[(t0 + i) * a.ldy + n] = f32_to_w16<kF16>(v);
-    }
+template <bool kGated, bool kF16>
+static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const void *w, int64_t ldw, cudaStream_t s) {
+  // gated: gate and up of 128 features and 128 rows a tile; else 128 outputs and 256 rows
+  constexpr int kMats = kGated ? 2 : 1, kNT = kGated ? 128 : 256;
+  DeviceInfo d;
+  if (!device_info(&d)) return MOE_ERR_CUDA;
+  CUtensorMap wm, x64, x16;
+  if (!gemm16_map(&wm, w, (int64_t)a.N * (kGated ? 2 : 1), a.K, ldw, 128, kF16) ||
+      !gemm16_map(&x64, x, a.rows, a.K, ldx, 64, kF16) || !gemm16_map(&x16, x, a.rows, a.K, ldx, 16, kF16)) {
+    set_cuda_error(cudaErrorInvalidValue);
+    return MOE_ERR_CUDA;
   }
+  a.mat_off = a.N;
+  a.nfb = (a.N + 127) / 128;
+  // equal chunks of rows
+  const int chunks = (a.rows + kNT - 1) / kNT;
+  a.nt = ((a.rows + chunks - 1) / chunks + 15) / 16 * 16;
+  const int64_t tiles = (int64_t)a.nfb * ((a.rows + a.nt - 1) / a.nt);
+  const int KB = (a.K + kG16BK - 1) / kG16BK;
+  a.splits = 1;
+  while (a.splits < 8 && tiles * a.splits * 2 <= d.sms && a.splits * 4 <= KB) a.splits *= 2;
+  const int grid = a.splits > 1 ? (int)tiles * a.splits : (int)(tiles < d.sms ? tiles : d.sms);
+  return gemm16_launch<false, kGated, kMats, kNT, kF16>(a, grid, wm, x64, x16, d.dev, s);
 }
 
 }  // namespace moe
@@ -59,7 +42,7 @@ extern "C" MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void 
   if (!x || !w || !y) return MOE_ERR_INVALID_ARG;
   if (ldx < K || ldw < K || ldy < N || (residual && ldr < N)) return MOE_ERR_INVALID_ARG;
   const int64_t ld_max = (int64_t)1 << 38;
-  if (ldx % 8 || ldw % 8 || ldx > ld_max || ldw > ld_max || ldy > ld_max || (residual && ldr > ld_max) || N > (1 << 30))
+  if (ldx % 8 || ldw % 8 || ldx > ld_max || ldw > ld_max || ldy > ld_max || (residual && ldr > ld_max) || N > (1 << 29))
     return MOE_ERR_UNSUPPORTED_SHAPE;
   const uintptr_t ymask = y_dtype == MOE_F32 ? 3 : 1;
   if (reinterpret_cast<uintptr_t>(x) % 16 || reinterpret_cast<uintptr_t>(w) % 16 ||
@@ -67,23 +50,21 @@ extern "C" MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void 
       reinterpret_cast<uintptr_t>(residual) % 2)
     return MOE_ERR_INVALID_ARG;
   if (residual == y && (y_dtype == MOE_F32 || ldr != ldy)) return MOE_ERR_INVALID_ARG;
-  LinearArgs a;
-  a.x = static_cast<const uint16_t *>(x);
-  a.w = static_cast<const uint16_t *>(w);
+  Gemm16Args a = {};
+  a.E = 1;
+  a.rows = T;
+  a.N = N;
+  a.K = K;
   a.bias = static_cast<const uint16_t *>(bias);
   a.residual = static_cast<const uint16_t *>(residual);
   a.y = y;
-  a.ldx = ldx;
-  a.ldw = ldw;
   a.ldr = ldr;
   a.ldy = ldy;
-  a.T = T;
-  a.N = N;
-  a.K = K;
   a.act = act;
-  a.gated = gated;
   a.y_f32 = y_dtype == MOE_F32;
-  const dim3 grid((unsigned)((N + 7) / 8), (unsigned)min((T + 3) / 4, 65535));
-  if (dtype == MOE_F16) return launch_pdl(linear_kernel<true>, grid, dim3(256), 0, as_stream(stream), a);
-  return launch_pdl(linear_kernel<false>, grid, dim3(256), 0, as_stream(stream), a);
+  a.err = device_error_word();
+  if (!a.err) return MOE_ERR_CUDA;
+  cudaStream_t s = as_stream(stream);
+  if (dtype == MOE_F16) return gated ? linear_gemm<true, true>(a, x, ldx, w, ldw, s) : linear_gemm<false, true>(a, x, ldx, w, ldw, s);
+  return gated ? linear_gemm<true, false>(a, x, ldx, w, ldw, s) : linear_gemm<false, false>(a, x, ldx, w, ldw, s);
 }

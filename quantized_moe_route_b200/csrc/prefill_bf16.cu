@@ -1,36 +1,6 @@
-// prefill_bf16.cu -- grouped expert FFN with bf16 experts.
-//
-// Two launches, one warp per row and output: h = SiLU(W_gate x) * W_up x,
-// then y = W_down h.
-#include "w16.cuh"
-
-namespace moe {
-
-__device__ __forceinline__ float pb16_dot(const uint16_t *a, const uint16_t *b, int n) {
-  float s = 0.f;
-  for (int c = threadIdx.x & 31; c < n; c += 32) s = __fmaf_rn(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-template <bool kGU>
-__global__ void __launch_bounds__(256) pb16_kernel(const uint16_t *w, const uint16_t *in, const int32_t *offsets,
-                                                   int E, int rows, int K, int N, uint16_t *out) {
-  grid_dep_wait();
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int r = blockIdx.y + blockIdx.z * 65535;
-  if (n >= N || r >= rows) return;
-  int e = 0;
-  while (e < E && !(min(max(offsets[e], 0), rows) <= r && r < min(max(offsets[e + 1], 0), rows))) ++e;
-  if (e == E) return;
-  const uint16_t *we = w + (size_t)e * (kGU ? 2 : 1) * N * K, *xr = in + (size_t)r * K;
-  float v = pb16_dot(xr, we + (size_t)n * K, K);
-  if (kGU) v = activate(v, MOE_ACT_SILU) * pb16_dot(xr, we + (size_t)(N + n) * K, K);
-  if ((threadIdx.x & 31) == 0) out[(size_t)r * N + n] = f32_to_bf16_bits(v);
-}
-
-}  // namespace moe
+// prefill_bf16.cu -- grouped expert FFN with bf16 experts: two launches of
+// the tensor-core product, h = SiLU(W_gate x) * W_up x and y = W_down h.
+#include "gemm16.cuh"
 
 using namespace moe;
 
@@ -55,10 +25,41 @@ extern "C" MOE_API moe_status moe_ffn_grouped_prefill_bf16(const moe_bf16_layer 
   if (reinterpret_cast<uintptr_t>(offsets) % 4) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = as_stream(stream);
   uint16_t *h = static_cast<uint16_t *>(ws);
-  const unsigned ry = (unsigned)min(rows, 65535), rz = (unsigned)((rows + 65534) / 65535);
-  moe_status st = launch_pdl(pb16_kernel<true>, dim3((F + 7) / 8, ry, rz), dim3(256), 0, s, layer->gate_up, x_perm,
-                             offsets, E, rows, H, F, h);
+  DeviceInfo d;
+  if (!device_info(&d)) return MOE_ERR_CUDA;
+  Gemm16Args a = {};
+  a.err = device_error_word();
+  if (!a.err) return MOE_ERR_CUDA;
+  CUtensorMap gum, dnm, x64, x16, h64, h16;
+  if (!gemm16_map(&gum, layer->gate_up, (int64_t)E * 2 * F, H, H, 128, false) ||
+      !gemm16_map(&dnm, layer->down, (int64_t)E * H, F, F, 128, false) ||
+      !gemm16_map(&x64, x_perm, rows, H, H, 64, false) || !gemm16_map(&x16, x_perm, rows, H, H, 16, false) ||
+      !gemm16_map(&h64, h, rows, F, F, 64, false) || !gemm16_map(&h16, h, rows, F, F, 16, false)) {
+    set_cuda_error(cudaErrorInvalidValue);
+    return MOE_ERR_CUDA;
+  }
+  a.offsets = offsets;
+  a.E = E;
+  a.rows = rows;
+  a.nt = 128;
+  a.splits = 1;
+  a.N = F;
+  a.K = H;
+  a.w_rows = 2 * F;
+  a.mat_off = F;
+  a.nfb = (F + 127) / 128;
+  a.y = h;
+  a.ldy = F;
+  a.act = MOE_ACT_SILU;
+  moe_status st = gemm16_launch<true, true, 2, 128, false>(a, d.sms, gum, x64, x16, d.dev, s);
   if (st != MOE_OK) return st;
-  return launch_pdl(pb16_kernel<false>, dim3((H + 7) / 8, ry, rz), dim3(256), 0, s, layer->down, (const uint16_t *)h,
-                    offsets, E, rows, F, H, y_perm);
+  a.N = H;
+  a.K = F;
+  a.w_rows = H;
+  a.mat_off = 128;
+  a.nfb = (H + 255) / 256;
+  a.y = y_perm;
+  a.ldy = H;
+  a.act = MOE_ACT_NONE;
+  return gemm16_launch<true, false, 2, 128, false>(a, d.sms, dnm, h64, h16, d.dev, s);
 }

@@ -4,6 +4,8 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace moe {
@@ -93,6 +95,11 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
 // M = 128, N = n.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// The same with bf16 or f16 operands.
+__host__ __device__ constexpr uint32_t idesc_16_f32(int n, bool f16) {
+  return idesc_bf16_f32(n) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
 }
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2,

@@ -29,7 +29,7 @@ def linear(x=P, ldx=64, w=P, ldw=64, T=4, N=32, K=64, dtype=moe.MOE_BF16, bias=N
     (INV, dict(bias=P + 1)), (INV, dict(residual=P + 1, ldr=32)),
     (INV, dict(residual=P, ldr=40, ldy=32)), (INV, dict(residual=P, ldr=32, y_dtype=moe.MOE_F32)),
     (SHAPE, dict(ldx=68)), (SHAPE, dict(ldw=65)), (SHAPE, dict(ldx=(1 << 38) + 8)),
-    (SHAPE, dict(N=(1 << 30) + 1, ldy=1 << 31)),
+    (SHAPE, dict(N=(1 << 29) + 1, ldy=1 << 31)),
     (moe.MOE_OK, dict(T=0)), (moe.MOE_OK, dict(N=0)), (moe.MOE_OK, dict(T=0, x=None, w=None, y=None)),
 ])
 def test_linear_refusals(want, kw):
