@@ -622,8 +622,9 @@ typedef struct {
  * workspace must not overlap in time.  After a call that raised the device
  * error word, zero-fill it again.  Co-residency as for moe_ffn_w4a16_decode.
  * Limits: 0 <= T <= 16, T * (k + shared) <= 256, 1 <= k <= min(Er, 32), k +
- * shared <= 32, E <= 1024, H % 64 == 0, F % 64 == 0.  Pointers to bf16
- * 16-byte aligned.  T == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * shared <= 32, E <= 1024, H % 64 == 0, F % 64 == 0, F <= 2^20, and the T rows
+ * of x have to fit in shared memory beside the weight stages: T * (2 H + 64)
+ * <= 166,000 bytes (16 tokens up to H = 5120).  Pointers to bf16 16-byte aligned.  T == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
  * WORKSPACE, CUDA.  A wait on the device that runs out raises
  * MOE_DEVERR_DECODE_H_WAIT or MOE_DEVERR_DECODE_ROUTER_WAIT.
  */

@@ -132,10 +132,10 @@ def _p(t):
 
 
 def _stream(stream):
-    if stream is None:
+    if stream is None:  # the current stream's handle (building a Stream object for it costs 3 us a call)
         import torch
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(status, where):
@@ -368,21 +368,26 @@ def moe_unpermute_combine(Y, w, y, inv=None, stream=None):
 
 
 # ---------------------------------------------------------------- 16-bit weights
-def _ld(t):
+def _refuse(why):
+    raise MoeError(MOE_ERR_INVALID_ARG, why)
+
+
+def _ld(t, rows, cols):
     """Row stride in elements of a [rows][cols] tensor whose rows are contiguous.  A single row has no next
     one: any stride that the call accepts will do."""
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise MoeError(MOE_ERR_INVALID_ARG, "row elements must be contiguous")
-    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        _refuse("row elements must be contiguous")
+    return ld if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _here(*tensors):
     """The tensors live on the current CUDA device, the one whose stream the call is enqueued on."""
     import torch
     dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2  # -1: a CPU tensor
-    if any(t is not None and t.get_device() != dev for t in tensors):
-        raise MoeError(MOE_ERR_INVALID_ARG, "tensors must be on the current CUDA device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse("tensors must be on the current CUDA device")
 
 
 def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False, stream=None):
@@ -391,18 +396,32 @@ def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False,
     be rows of wider buffers (row strides of x and w in multiples of 8 elements)."""
     import torch
     T, K = x.shape
-    N = y.shape[1]
-    if (w.shape != ((2 * N if gated else N), K) or y.shape[0] != T
-            or (bias is not None and (bias.numel() != w.shape[0] or not bias.is_contiguous()))
-            or (residual is not None and residual.shape != y.shape)
-            or any(t is not None and t.dtype != x.dtype for t in (w, bias, residual))
-            or y.dtype not in (x.dtype, torch.float32) or x.element_size() != 2):
-        raise MoeError(MOE_ERR_INVALID_ARG, "moe_linear")
+    Ty, N = y.shape
+    rows = 2 * N if gated else N
+    dtype, ydtype = x.dtype, y.dtype
+    if w.shape != (rows, K) or Ty != T or w.dtype != dtype or x.element_size() != 2:
+        _refuse("moe_linear: shapes or types of x, w and y")
+    dt = MOE_F16 if dtype == torch.float16 else MOE_BF16
+    if ydtype == dtype:
+        ydt = dt
+    elif ydtype == torch.float32:
+        ydt = MOE_F32
+    else:
+        _refuse("moe_linear: type of y")
+    bp, rp, ldr = None, None, 0
+    if bias is not None:
+        if bias.shape != (rows,) or bias.dtype != dtype or not bias.is_contiguous():
+            _refuse("moe_linear: bias")
+        bp = bias.data_ptr()
+    if residual is not None:
+        if residual.shape != y.shape or residual.dtype != dtype:
+            _refuse("moe_linear: residual")
+        rp, ldr = residual.data_ptr(), _ld(residual, T, N)
     _here(x, w, y, bias, residual)
-    dt = MOE_F16 if x.dtype == torch.float16 else MOE_BF16
-    _check(lib().moe_linear(x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), T, N, K, dt, _p(bias), act, int(gated),
-                            _p(residual), 0 if residual is None else _ld(residual), y.data_ptr(), _ld(y),
-                            MOE_F32 if y.dtype == torch.float32 else dt, _stream(stream)), "moe_linear")
+    status = (_lib or lib()).moe_linear(x.data_ptr(), _ld(x, T, K), w.data_ptr(), _ld(w, rows, K), T, N, K, dt, bp, act,
+                                        1 if gated else 0, rp, ldr, y.data_ptr(), _ld(y, T, N), ydt, _stream(stream))
+    if status != MOE_OK:
+        raise MoeError(status, "moe_linear")
 
 
 def make_bf16_layer(E, H, F, gate_up, down) -> moe_bf16_layer:

@@ -1,72 +1,606 @@
-// decode_bf16.cu -- one MoE layer with bf16 experts for up to 16 tokens.
+// decode_bf16.cu -- one MoE layer with bf16 experts for up to 16 tokens, in
+// one launch: the router, the routing, every selected expert's gate/up,
+// SwiGLU and down projection, the shared expert, the combine and the
+// residual.
 //
-// Four launches: the router's logits (one warp per token and expert), the
-// routing (one warp per token), h (one warp per routed row and feature), and
-// the down projection with the combine (one warp per token and output).
+// A decode step reads each selected expert's weights once (6 H F bytes) and
+// does little else, so the kernel is a stream: a persistent grid, one CTA per
+// SM, whose producer warp copies weight rows as they lie in memory
+// (cp.async.bulk, one row piece a lane) through a ring of ~17 KB stages, and
+// 16 consumer warps that each take whole units of work from it, so no barrier
+// between warps sits on the stream.
+//   phase A  unit = 4 or 8 features of one expert (their gate and up rows, all
+//            H inputs).  Units go round the CTAs; h is published as 8-byte
+//            words {fp32 h, call epoch} (single-copy atomic: a reader polls
+//            the words themselves, no fence or counter on the path).
+//   phase B  a CTA owns R output channels (H / CTAs, at most 16) and runs
+//            every selected expert's rows of them, one warp per expert: all k
+//            rows of a token meet in the CTA's shared memory, so the combine
+//            needs no second handoff.  The producer runs ahead: these weights
+//            do not depend on h and are loaded while h is still on its way.
+// Dot products run on m16n8k16 tensor-core instructions with the weight rows
+// as A and the tokens as B.  A sum over k may take k in any order, so lane
+// (g, t) reads 16 consecutive bytes of its row per 32 inputs and uses them as
+// the fragments of two instructions; rows are 64 bytes (mod 128) apart in
+// shared memory, so eight lanes' 16-byte reads touch every bank once.  The
+// down projection takes h as a pair of bf16 values (hi + lo, 16 significant
+// bits): the second product is free in a kernel bound by its stream.
+//
+// The router's logits are computed over the grid (each CTA its experts' rows,
+// K split over the warps, partial sums added in warp order), published as
+// words {logit, epoch}, and every CTA routes for itself.  Every CTA is
+// resident (cooperative launch) and every wait is bounded.
+#include <atomic>
+
+#include "decode_common.cuh"
+#include "decode_items.cuh"
 #include "route.cuh"
 #include "w16.cuh"
 
 namespace moe {
 
-constexpr size_t kB16CtrlBytes = 4096;
+constexpr int kB16Warps = 16;                         // consumers; one more warp produces
+constexpr int kB16Threads = (kB16Warps + 1) * 32;
+constexpr int kB16KC = 512;                           // inputs of a 16-row stage (an 8-row stage: twice that)
+constexpr uint32_t kB16Stage = 16 * (kB16KC * 2 + 64);  // bytes of a stage
+constexpr int kB16MaxStages = 12;
+constexpr int kB16MaxF = 1 << 20;
+constexpr int kB16MaxX = 166000;                      // bytes of x rows that fit beside two stages
+constexpr size_t kB16CtrlBytes = 4096;                // workspace head: epoch, done counter
+constexpr uint32_t kB16Polls = 1u << 22;              // bound of a poll loop (of >= 32 ns sleeps)
+constexpr uint32_t kB16BarPolls = 1u << 19;           // bound of a barrier wait (polls suspend for some us)
 
 struct DecodeBf16Args {
   const uint16_t *gu, *dn, *x, *wr, *sg, *residual;
-  const float *logits;
-  float *logits_ws, *w;  // w: routing weights [T][k]
-  float *sgate;          // [T] shared gate
-  int32_t *idx;          // [T][k]
-  float *h;  // [T (k + shared)][F]
+  float *logits;             // [T][Er]: the input, or with wr an optional output
+  unsigned long long *hbuf;  // [T kk][F] words {fp32 h, epoch}
+  unsigned long long *lbuf;  // [T][Er + 1] words {fp32 logit, epoch}; entry Er: the shared expert's gate
+  unsigned int *ctrl;        // [0] last epoch, [1] CTAs done
   uint16_t *y;
-  int T, k, shared, E, H, F;
+  int32_t *idx;
+  float *w;
+  int *err;
+  int T, kk, shared, E, H, F;  // kk: rows per token (k + shared)
+  int nst;                     // ring stages
+  uint32_t hb_bytes;           // per-warp h buffer
 };
 
-__device__ __forceinline__ float warp_dot(const uint16_t *a, const uint16_t *b, int n) {
-  float s = 0.f;
-  for (int c = threadIdx.x & 31; c < n; c += 32) s = __fmaf_rn(bf16_bits_to_f32(a[c]), bf16_bits_to_f32(b[c]), s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+struct B16Smem {
+  uint32_t x, rows, tables, total;  // byte offsets; the ring is at 0
+};
+__host__ __device__ inline uint32_t b16_hb_bytes(int T) {  // one token's (two tokens') 512 h values as hi + lo, or 8 x 64
+  return T == 1 ? 2176u : 4352u;
+}
+__host__ __device__ inline B16Smem b16_layout(int T, int kk, int H, int nst) {
+  B16Smem L;
+  L.x = (uint32_t)nst * kB16Stage;
+  const uint32_t xb = (uint32_t)T * (uint32_t)(H * 2 + 64), hb = kB16Warps * b16_hb_bytes(T);
+  L.rows = L.x + (xb > hb ? xb : hb);  // x in phase A, the warps' h in phase B
+  L.tables = L.rows + (uint32_t)(T * kk) * 64u;
+  L.total = L.tables + 32 * 4 + 256 * 4 + 256 * 16 + 256 * 4 + 256 * 4 + 256 * 4 + 2 * 8 * kB16MaxStages + 64;
+  return L;
 }
 
-__global__ void __launch_bounds__(256) db16_logits_kernel(DecodeBf16Args a) {
-  grid_dep_wait();
-  const int Er = a.E - a.shared, e = blockIdx.x * 8 + (threadIdx.x >> 5), t = blockIdx.y;
-  if (e > Er || (e < Er && !a.wr) || (e == Er && !a.sg)) return;
-  const float v = warp_dot(a.x + (size_t)t * a.H, e < Er ? a.wr + (size_t)e * a.H : a.sg, a.H);
-  if ((threadIdx.x & 31) == 0) {
-    if (e < Er) a.logits_ws[(size_t)t * Er + e] = v;
-    else a.sgate[t] = sigmoid_f32(v);
+__device__ __forceinline__ void b16_consumer_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void st_relaxed_u64(unsigned long long *p, unsigned long long v) {
+  asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ void ld_relaxed_u64x2(const unsigned long long *p, unsigned long long &a, unsigned long long &b) {
+  asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p) : "memory");
+}
+// the n-th set bit of m (n < popc(m))
+__device__ __forceinline__ int nth_bit(uint32_t m, int n) {
+  for (int i = 0; i < n; ++i) m &= m - 1u;
+  return __ffs(m) - 1;
+}
+
+// kRows: weight rows of a phase A unit, half gate and half up (8: up to 8
+// tokens; 16: two token columns of 8).  PER: logits per lane in the routing.
+template <int kRows, int PER>
+__global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16Args a) {
+  constexpr int NB = kRows == 16 ? 2 : 1;        // token blocks of 8
+  constexpr int FPU = kRows / 2;                 // features of a unit
+  constexpr int KCA = kRows == 16 ? kB16KC : 2 * kB16KC;
+  constexpr uint32_t pitchA = KCA * 2 + 64, pitchB = kB16KC * 2 + 64;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const B16Smem L = b16_layout(a.T, a.kk, a.H, a.nst);
+  float *rowbuf = reinterpret_cast<float *>(smem + L.rows);            // [T kk][16]
+  uint32_t *emask = reinterpret_cast<uint32_t *>(smem + L.tables);     // [32] expert presence bits
+  uint32_t *tokmask = emask + 32;                                      // [256] tokens of a slot
+  uint8_t *slot_j = reinterpret_cast<uint8_t *>(tokmask + 256);        // [256][16] row of (slot, token) within the token
+  int *slot_expert = reinterpret_cast<int *>(slot_j + 256 * 16);       // [256]
+  int *ridx = slot_expert + 256;                                       // [256] expert of a row
+  float *rw = reinterpret_cast<float *>(ridx + 256);                   // [256] weight of a row
+  uint64_t *full = reinterpret_cast<uint64_t *>(rw + 256);
+  uint64_t *empty = full + kB16MaxStages;
+  volatile int *misc = reinterpret_cast<volatile int *>(empty + kB16MaxStages);  // [0] abort, [1] epoch, [2] stages issued
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int T = a.T, kk = a.kk, H = a.H, F = a.F, Er = a.E - a.shared, G = gridDim.x, nst = a.nst;
+  const uint32_t xpitch = (uint32_t)(H * 2 + 64);
+
+  if (tid == 0) {
+    for (int s = 0; s < nst; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    misc[0] = 0;
+    misc[2] = 0;
+    fence_mbar_init();
+  }
+  if (tid < 32) emask[tid] = 0u;
+  if (tid < 256) tokmask[tid] = 0u;
+  pdl_wait();
+  if (tid == kB16Threads - 1) {
+    const unsigned int ep = a.ctrl[0] + 1u;  // this call's epoch; never 0 (zeroed words never match)
+    misc[1] = (int)(ep == 0u ? 1u : ep);
+  }
+  if (warp < kB16Warps) {
+    for (int v = tid; v < T * (H / 8); v += kB16Warps * 32) {
+      const int t = v / (H / 8), c = v - t * (H / 8);
+      cp_async_16(smem + L.x + (size_t)t * xpitch + 16 * c, a.x + (size_t)t * H + 8 * c);
+    }
+    cp_async_commit();
+  }
+  auto fail = [&](int code) {
+    atomicExch(a.err, code);
+    misc[0] = 1;
+  };
+
+  // ---- router: rows blockIdx.x + G i of {wr, shared gate}, 16 at a time
+  const bool have_rows = a.wr != nullptr || a.sg != nullptr;
+  if (have_rows) {
+    const int lo = a.wr ? 0 : Er, hi = a.sg ? Er + 1 : Er;  // experts' rows, then the gate's
+    float *part = reinterpret_cast<float *>(smem);          // the ring is idle: [16 warps][16 rows][16 tokens]
+    for (int e0 = lo + (int)blockIdx.x; e0 < hi; e0 += 16 * G) {
+      const uint16_t *r0 = nullptr, *r1 = nullptr;  // this lane's rows g and g + 8
+      const int ea = e0 + g * G, eb = e0 + (g + 8) * G;
+      if (ea < hi) r0 = ea < Er ? a.wr + (size_t)ea * H : a.sg;
+      if (eb < hi) r1 = eb < Er ? a.wr + (size_t)eb * H : a.sg;
+      float d[2][4] = {};
+      const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+      for (int b = warp; b < H / 32 && warp < kB16Warps; b += kB16Warps) {
+        const int c = 32 * b + 8 * t4;
+        const uint4 w0 = r0 ? *reinterpret_cast<const uint4 *>(r0 + c) : z;
+        const uint4 w1 = r1 ? *reinterpret_cast<const uint4 *>(r1 + c) : z;
+        const uint4 q0 = g < T ? *reinterpret_cast<const uint4 *>(a.x + (size_t)g * H + c) : z;
+        const uint4 q1 = g + 8 < T ? *reinterpret_cast<const uint4 *>(a.x + (size_t)(g + 8) * H + c) : z;
+        const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
+        mma_bf16_16816(d[0], f0, q0.x, q0.y);
+        mma_bf16_16816(d[0], f1, q0.z, q0.w);
+        if (NB == 2) {
+          mma_bf16_16816(d[1], f0, q1.x, q1.y);
+          mma_bf16_16816(d[1], f1, q1.z, q1.w);
+        }
+      }
+      if (warp < kB16Warps) {
+        float *p = part + warp * 256;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int n = nb * 8 + 2 * t4;
+          p[g * 16 + n] = d[nb][0];
+          p[g * 16 + n + 1] = d[nb][1];
+          p[(g + 8) * 16 + n] = d[nb][2];
+          p[(g + 8) * 16 + n + 1] = d[nb][3];
+        }
+      }
+      __syncthreads();
+      if (tid < 256) {
+        const int r = tid >> 4, t = tid & 15, e = e0 + r * G;
+        if (t < T && e < hi) {
+          float v = 0.f;
+#pragma unroll
+          for (int w = 0; w < kB16Warps; ++w) v += part[w * 256 + tid];
+          st_relaxed_u64(a.lbuf + (size_t)t * (Er + 1) + e,
+                         ((unsigned long long)__float_as_uint(v) << 32) | (unsigned int)misc[1]);
+          if (e < Er && a.logits) a.logits[(size_t)t * Er + e] = v;
+          __threadfence();  // every CTA polls these words: push them out now
+        }
+      }
+      __syncthreads();
+    }
+    fence_proxy_async_smem();  // the ring's next writers are the weight copies
+  }
+  __syncthreads();  // barrier initialisation, table clears, the epoch
+  const unsigned int epoch = (unsigned int)misc[1];
+
+  // ---- routing: warp t routes token t
+  if (warp < T) {
+    const int k = kk - a.shared;
+    const unsigned long long *lw = a.lbuf + (size_t)warp * (Er + 1);
+    uint32_t key[PER];
+    if (a.wr) {
+      unsigned long long wv[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) wv[i] = lane + 32 * i < Er ? ld_relaxed_u64(lw + lane + 32 * i) : 0ull;
+      uint32_t spins = 0;
+      while (true) {  // reload all of the lane's words still from an earlier call
+        uint32_t pending = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (lane + 32 * i < Er && (unsigned int)wv[i] != epoch) pending |= 1u << i;
+        if (!pending) break;
+        if (++spins > kB16Polls) {
+          fail(DEVERR_DECODE_ROUTER_WAIT);
+          break;
+        }
+        __nanosleep(32);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if ((pending >> i) & 1u) wv[i] = ld_relaxed_u64(lw + lane + 32 * i);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = lane + 32 * i < Er ? route_key(__uint_as_float((unsigned int)(wv[i] >> 32))) : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = lane + 32 * i < Er ? route_key(a.logits[(size_t)warp * Er + lane + 32 * i]) : 0u;
+    }
+    int j_idx;
+    float j_w;
+    route_token_keys<PER>(key, k, &j_idx, &j_w);
+    j_idx = min(max(j_idx, 0), Er - 1);  // (NaN logits are outside the contract; stay memory safe)
+    if (lane < k && blockIdx.x == 0 && a.idx) {
+      a.idx[warp * k + lane] = j_idx;
+      a.w[warp * k + lane] = j_w;
+    }
+    if (a.shared && lane == k) {
+      j_idx = Er;
+      j_w = 1.0f;
+      if (a.sg) {
+        unsigned long long v = ld_relaxed_u64(lw + Er);
+        for (uint32_t spins = 0; (unsigned int)v != epoch; v = ld_relaxed_u64(lw + Er)) {
+          if (++spins > kB16Polls) {
+            fail(DEVERR_DECODE_ROUTER_WAIT);
+            break;
+          }
+          __nanosleep(32);
+        }
+        j_w = sigmoid_f32(__uint_as_float((unsigned int)(v >> 32)));
+      }
+    }
+    if (lane < kk) {
+      ridx[warp * kk + lane] = j_idx;
+      rw[warp * kk + lane] = j_w;
+      atomicOr(&emask[j_idx >> 5], 1u << (j_idx & 31));
+    }
+  }
+  cp_async_wait_all();  // this thread's part of x
+  __syncthreads();
+  pdl_launch_dependents();
+  // slots: the selected experts in increasing id; every warp scans the presence words for itself
+  const uint32_t em = emask[lane];
+  const int incl = warp_inclusive_scan(__popc(em)), ebase = incl - __popc(em);
+  const int U = __shfl_sync(0xffffffffu, incl, 31);
+  const int UA = F / FPU, nUnits = U * UA;
+  const int myUnits = (int)blockIdx.x < nUnits ? (nUnits - 1 - (int)blockIdx.x) / G + 1 : 0;
+  const int CA = (H + KCA - 1) / KCA, CB = (F + kB16KC - 1) / kB16KC;
+  const int nA = myUnits * CA;  // stages of phase A
+  const int per_cta = (H + 16 * G - 1) / (16 * G), R = (H + per_cta * G - 1) / (per_cta * G);
+  const int nStrips = (H + R - 1) / R;
+  const int myStrips = (int)blockIdx.x < nStrips ? (nStrips - 1 - (int)blockIdx.x) / G + 1 : 0;
+
+  auto wait_bar = [&](uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kB16BarPolls; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (misc[0]) return false;
+    }
+    fail(DEVERR_DECODE_H_WAIT);
+    return false;
+  };
+  // Wait for stage use `ord`.  A warp may be several uses of a stage ahead of
+  // its barrier, whose parity alone would then say "done" for an earlier use,
+  // so the producer's count comes first: once use `ord` is issued, every
+  // earlier use of its stage has been consumed.
+  auto wait_full = [&](int ord) {
+    for (uint32_t i = 0; misc[2] <= ord; ++i) {
+      if (misc[0]) return false;
+      if (i > kB16Polls) {
+        fail(DEVERR_DECODE_H_WAIT);
+        return false;
+      }
+      __nanosleep(32);
+    }
+    return wait_bar(&full[ord % nst], (ord / nst) & 1);
+  };
+
+  if (warp == kB16Warps) {
+    // ------------------------------------------------------------ producer
+    {
+      uint32_t m = em;
+      int b = ebase;
+      while (m) {  // slots in order of expert id
+        slot_expert[b++] = 32 * lane + __ffs(m) - 1;
+        m &= m - 1u;
+      }
+    }
+    __syncwarp();
+    const uint64_t pol = policy_evict_first();
+    int ord = 0;
+    bool ok = true;
+    // one row piece per lane: nrows rows of `bytes` bytes, src this lane's row
+    auto put = [&](const uint16_t *src, int nrows, uint32_t bytes, uint32_t pitch) {
+      const int s = ord % nst;
+      if (!__all_sync(0xffffffffu, wait_bar(&empty[s], ((ord / nst) & 1) ^ 1))) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[s], bytes * (uint32_t)nrows);
+        misc[2] = ord + 1;
+      }
+      __syncwarp();
+      if (lane < nrows) bulk_g2s_evict_first(smem + (size_t)s * kB16Stage + lane * pitch, src, bytes, &full[s], pol);
+      ++ord;
+      return true;
+    };
+    for (int q = 0; q < myUnits && ok; ++q) {
+      const int unit = blockIdx.x + q * G, slot = unit / UA, f0 = (unit - slot * UA) * FPU;
+      const int row = lane < FPU ? f0 + lane : F + f0 + (lane & (FPU - 1));
+      const uint16_t *src = a.gu + ((size_t)slot_expert[slot] * 2 * F + row) * H;
+      for (int c = 0; c < CA && ok; ++c) ok = put(src + c * KCA, kRows, 2u * (uint32_t)min(KCA, H - c * KCA), pitchA);
+    }
+    for (int si = 0; si < myStrips && ok; ++si) {
+      const int row0 = (blockIdx.x + si * G) * R, nr = min(R, H - row0);
+      for (int u = 0; u < U && ok; ++u) {
+        const uint16_t *src = a.dn + ((size_t)slot_expert[u] * H + row0 + min(lane, nr - 1)) * F;
+        for (int c = 0; c < CB && ok; ++c)
+          ok = put(src + c * kB16KC, nr, 2u * (uint32_t)min(kB16KC, F - c * kB16KC), pitchB);
+      }
+    }
+    // the last copies issued into each stage land before the CTA leaves, also
+    // when the consumers gave up
+    if (lane == 0)
+      for (int o = max(0, ord - nst); o < ord; ++o) mbar_wait_bounded(&full[o % nst], (o / nst) & 1, 1u << 20);
+  } else {
+    // ------------------------------------------------------------ consumers
+    if (tid < T * kk) {
+      const int t = tid / kk, e = ridx[tid];
+      int slot = 0;  // rank of e among the selected
+      for (int w = 0; w < (e >> 5); ++w) slot += __popc(emask[w]);
+      slot += __popc(emask[e >> 5] & ((1u << (e & 31)) - 1u));
+      atomicOr(&tokmask[slot], 1u << t);
+      slot_j[slot * 16 + t] = (uint8_t)(tid - t * kk);
+    }
+    b16_consumer_sync();
+    bool ok = true;
+    // ---- phase A
+    const uint32_t ring = smem_u32(smem), xs = smem_u32(smem + L.x);
+    for (int q = warp; q < myUnits && ok; q += kB16Warps) {
+      const int unit = blockIdx.x + q * G, slot = unit / UA, f0 = (unit - slot * UA) * FPU;
+      const uint32_t mask = tokmask[slot];
+      const int ntok = __popc(mask);
+      uint32_t xa[NB];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int n = nb * 8 + g;
+        xa[nb] = xs + (uint32_t)nth_bit(mask, n < ntok ? n : 0) * xpitch + 16u * t4;
+      }
+      const bool two = NB == 2 && ntok > 8;
+      float acc[NB][2][4] = {};
+      for (int c = 0; c < CA; ++c) {
+        const int o = q * CA + c, s = o % nst;
+        if (!__all_sync(0xffffffffu, wait_full(o))) {
+          ok = false;
+          break;
+        }
+        const uint32_t wa = ring + (uint32_t)s * kB16Stage + (uint32_t)g * pitchA + 16u * t4;
+        const int nblk = min(KCA, H - c * KCA) / 32;
+        const uint32_t xo = (uint32_t)(c * KCA * 2);
+#pragma unroll 4
+        for (int b = 0; b < nblk; ++b) {
+          const uint4 w0 = lds_u4(wa + 64 * b);
+          const uint4 w1 = kRows == 16 ? lds_u4(wa + 8 * pitchA + 64 * b) : make_uint4(0, 0, 0, 0);
+          const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            if (nb == 1 && !two) continue;
+            const uint4 v = lds_u4(xa[nb] + xo + 64 * b);
+            mma_bf16_16816(acc[nb][0], f0r, v.x, v.y);
+            mma_bf16_16816(acc[nb][1], f1r, v.z, v.w);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = acc[nb][0][i] + acc[nb][1][i];
+        if (kRows == 8) {  // rows 0-3 gate, 4-7 up: the partner is 16 lanes up
+          v[2] = __shfl_down_sync(0xffffffffu, v[0], 16);
+          v[3] = __shfl_down_sync(0xffffffffu, v[1], 16);
+        }
+        if (kRows == 8 && g >= 4) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = nb * 8 + 2 * t4 + i;
+          if (n < ntok) {
+            const int t = nth_bit(mask, n);
+            const float h = activate(v[i], MOE_ACT_SILU) * v[2 + i];
+            st_relaxed_u64(a.hbuf + (size_t)(t * kk + slot_j[slot * 16 + t]) * F + f0 + g,
+                           ((unsigned long long)__float_as_uint(h) << 32) | epoch);
+          }
+        }
+      }
+    }
+    b16_consumer_sync();  // x is consumed: its space holds the warps' h now
+
+    // ---- phase B
+    const uint32_t hb = xs + (uint32_t)warp * a.hb_bytes;
+    uint8_t *hbp = smem + L.x + (size_t)warp * a.hb_bytes;
+    for (int si = 0; si < myStrips; ++si) {
+      const int row0 = (blockIdx.x + si * G) * R, nr = min(R, H - row0);
+      const int J = si * U;
+      for (int u = (warp - J % kB16Warps + kB16Warps) % kB16Warps; u < U && ok; u += kB16Warps) {
+        const uint32_t mask = tokmask[u];
+        const int ntok = __popc(mask);
+        float acc[2][2][4] = {};
+        for (int c = 0; c < CB && ok; ++c) {
+          const int o = nA + (J + u) * CB + c, s = o % nst, cc = min(kB16KC, F - c * kB16KC);
+          const uint32_t wa = ring + (uint32_t)s * kB16Stage + (uint32_t)g * pitchB + 16u * t4;
+          bool landed = false;
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb) {
+            if (8 * nb >= ntok) break;
+            const int m = min(8, ntok - 8 * nb);  // tokens of this block
+            int fc = kB16KC;                      // inputs whose h fits the warp's buffer
+            while ((uint32_t)(m * (fc * 2 + 64) * 2) > a.hb_bytes) fc >>= 1;
+            for (int k1 = 0; k1 < cc && ok; k1 += fc) {
+              const int kc = min(fc, cc - k1), per = kc / 64;  // 16-byte word pairs of a token per lane
+              const uint32_t hp = (uint32_t)(kc * 2 + 64);     // bytes between tokens
+              const uint32_t lo_off = (uint32_t)m * hp;
+              __syncwarp();
+              for (int i0 = 0; i0 < m * per && ok; i0 += 8) {
+                unsigned long long wv[8][2];
+                uint32_t src[8];  // in pairs of words (at most 256 rows of 2^20)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const int n = min((i0 + i) / per, m - 1), p = (i0 + i) % per;
+                  const int t = nth_bit(mask, 8 * nb + n);
+                  src[i] = (uint32_t)(((t * kk + slot_j[u * 16 + t]) * F + c * kB16KC + k1) / 2 + p * 32 + lane);
+                }
+                uint32_t spins = 0;
+                while (true) {
+                  bool mine = true;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (i0 + i < m * per) ld_relaxed_u64x2(a.hbuf + 2 * (size_t)src[i], wv[i][0], wv[i][1]);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (i0 + i < m * per && ((unsigned int)wv[i][0] != epoch || (unsigned int)wv[i][1] != epoch)) mine = false;
+                  if (__all_sync(0xffffffffu, mine)) break;
+                  ++spins;
+                  if (spins > kB16Polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
+                  if (__any_sync(0xffffffffu, spins > kB16Polls || misc[0])) {
+                    ok = false;
+                    break;
+                  }
+                  __nanosleep(64);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  if (i0 + i >= m * per) break;
+                  const int n = (i0 + i) / per, p = (i0 + i) % per;
+                  const float h0 = __uint_as_float((uint32_t)(wv[i][0] >> 32)), h1 = __uint_as_float((uint32_t)(wv[i][1] >> 32));
+                  const uint32_t hi = cvt_bf16x2(h0, h1);
+                  const uint32_t lo = cvt_bf16x2(h0 - __uint_as_float(hi << 16), h1 - __uint_as_float(hi & 0xFFFF0000u));
+                  const uint32_t at = (uint32_t)n * hp + (uint32_t)(p * 32 + lane) * 4u;
+                  *reinterpret_cast<uint32_t *>(hbp + at) = hi;
+                  *reinterpret_cast<uint32_t *>(hbp + lo_off + at) = lo;
+                }
+              }
+              __syncwarp();
+              if (ok && !landed) {
+                ok = __all_sync(0xffffffffu, wait_full(o));
+                landed = true;
+              }
+              if (!ok) break;
+              const uint32_t ha = hb + (uint32_t)min(g, m - 1) * hp + 16u * t4;
+              const uint32_t wk = wa + (uint32_t)k1 * 2u;
+#pragma unroll 4
+              for (int b = 0; b < kc / 32; ++b) {
+                const uint4 w0 = lds_u4(wk + 64 * b), w1 = lds_u4(wk + 8 * pitchB + 64 * b);
+                const uint4 vh = lds_u4(ha + 64 * b), vl = lds_u4(ha + lo_off + 64 * b);
+                const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+                mma_bf16_16816(acc[nb][0], f0r, vh.x, vh.y);
+                mma_bf16_16816(acc[nb][1], f1r, vh.z, vh.w);
+                mma_bf16_16816(acc[nb][0], f0r, vl.x, vl.y);
+                mma_bf16_16816(acc[nb][1], f1r, vl.z, vl.w);
+              }
+            }
+          }
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&empty[s]);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int n = nb * 8 + 2 * t4 + i;
+            if (n < ntok) {
+              const int t = nth_bit(mask, n);
+              float *rb = rowbuf + (t * kk + slot_j[u * 16 + t]) * 16;
+              rb[g] = acc[nb][0][i] + acc[nb][1][i];
+              rb[g + 8] = acc[nb][0][2 + i] + acc[nb][1][2 + i];
+            }
+          }
+      }
+      b16_consumer_sync();  // every expert's rows of this strip are in rowbuf
+      if (!misc[0]) {
+        for (int v = tid; v < T * nr; v += kB16Warps * 32) {
+          const int t = v / nr, o = v - t * nr;
+          float s = 0.f;
+          for (int j = 0; j < kk; ++j) s = __fmaf_rn(rw[t * kk + j], rowbuf[(t * kk + j) * 16 + o], s);
+          const size_t at = (size_t)t * H + row0 + o;
+          if (a.residual) s += bf16_bits_to_f32(a.residual[at]);
+          a.y[at] = f32_to_bf16_bits(s);
+        }
+      }
+      b16_consumer_sync();  // rowbuf is free for the next strip
+    }
+  }
+  __syncthreads();
+  // the last CTA out records this call's epoch for the next call
+  if (tid == 0) {
+    const unsigned int done = atomicAdd(&a.ctrl[1], 1u);
+    if (done == (unsigned int)G - 1u) {
+      a.ctrl[0] = epoch;
+      a.ctrl[1] = 0u;
+      __threadfence();
+    }
   }
 }
 
-__global__ void __launch_bounds__(256) db16_h_kernel(DecodeBf16Args a) {
-  grid_dep_wait();
-  const int kk = a.k + a.shared, f = blockIdx.x * 8 + (threadIdx.x >> 5), r = blockIdx.y, t = r / kk, j = r % kk;
-  if (f >= a.F) return;
-  const int e = j < a.k ? a.idx[t * a.k + j] : a.E - 1;
-  const uint16_t *w = a.gu + (size_t)e * 2 * a.F * a.H, *xr = a.x + (size_t)t * a.H;
-  const float g = warp_dot(xr, w + (size_t)f * a.H, a.H), u = warp_dot(xr, w + (size_t)(a.F + f) * a.H, a.H);
-  if ((threadIdx.x & 31) == 0) a.h[(size_t)r * a.F + f] = activate(g, MOE_ACT_SILU) * u;
-}
-
-__global__ void __launch_bounds__(256) db16_y_kernel(DecodeBf16Args a) {
-  grid_dep_wait();
-  const int kk = a.k + a.shared, c = blockIdx.x * 8 + (threadIdx.x >> 5), t = blockIdx.y;
-  if (c >= a.H) return;
-  float acc = 0.f;
-  for (int j = 0; j < kk; ++j) {
-    const int e = j < a.k ? a.idx[t * a.k + j] : a.E - 1;
-    const float *h = a.h + ((size_t)t * kk + j) * a.F;
-    const uint16_t *d = a.dn + ((size_t)e * a.H + c) * a.F;
-    float v = 0.f;
-    for (int f = threadIdx.x & 31; f < a.F; f += 32) v = __fmaf_rn(h[f], bf16_bits_to_f32(d[f]), v);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    acc += (j < a.k ? a.w[t * a.k + j] : a.sg ? a.sgate[t] : 1.0f) * v;
+template <int kRows, int PER>
+static moe_status decode_bf16_launch(DecodeBf16Args &a, cudaStream_t stream) {
+  auto kern = decode_bf16_kernel<kRows, PER>;
+  int dev = 0, sms = 0, smem_max = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+  const uint32_t cap = (uint32_t)smem_max;
+  a.hb_bytes = b16_hb_bytes(a.T);
+  a.nst = kB16MaxStages;
+  while (a.nst > 2 && b16_layout(a.T, a.kk, a.H, a.nst).total > cap) --a.nst;
+  const B16Smem L = b16_layout(a.T, a.kk, a.H, a.nst);
+  if (L.total > cap) return MOE_ERR_UNSUPPORTED_SHAPE;
+  static std::atomic<int> per_sm[64];  // per device: the shared-memory opt-in and the CTAs per SM it allows
+  if (dev < 0 || dev >= 64) {
+    set_cuda_error(cudaErrorInvalidDevice);
+    return MOE_ERR_CUDA;
   }
-  if (a.residual) acc += bf16_bits_to_f32(a.residual[(size_t)t * a.H + c]);
-  if ((threadIdx.x & 31) == 0) a.y[(size_t)t * a.H + c] = f32_to_bf16_bits(acc);
+  if (per_sm[dev].load(std::memory_order_acquire) == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cap);
+    int occ = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, kB16Threads, cap);
+    if (e != cudaSuccess) {
+      set_cuda_error(e);
+      return MOE_ERR_CUDA;
+    }
+    if (occ < 1) return MOE_ERR_UNSUPPORTED_SHAPE;
+    per_sm[dev].store(occ, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(sms * per_sm[dev].load(std::memory_order_acquire));
+  cfg.blockDim = dim3(kB16Threads);
+  cfg.dynamicSmemBytes = L.total;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) {
+    set_cuda_error(e);
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
 }
 
 }  // namespace moe
@@ -76,7 +610,7 @@ using namespace moe;
 extern "C" MOE_API size_t moe_decode_layer_bf16_workspace_bytes(int T, int k, int shared, int E, int H, int F) {
   if (T <= 0 || k <= 0 || shared < 0 || shared > 1 || E <= shared || H <= 0 || F <= 0) return 0;
   // control words, h words of every routed row, logit words of every expert
-  return kB16CtrlBytes + sizeof(unsigned long long) * ((size_t)T * (k + shared) * F + (size_t)T * E);
+  return kB16CtrlBytes + sizeof(unsigned long long) * ((size_t)T * (k + shared) * F + (size_t)T * (E + 1));
 }
 
 extern "C" MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer, const uint16_t *x, const uint16_t *wr,
@@ -87,7 +621,9 @@ extern "C" MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer,
   if (!layer || T < 0 || k <= 0 || shared < 0 || shared > 1) return MOE_ERR_INVALID_ARG;
   const int E = layer->E, H = layer->H, F = layer->F, kk = k + shared, Er = E - shared;
   if (Er <= 0 || H <= 0 || F <= 0 || k > Er || (shared_gate && !shared)) return MOE_ERR_INVALID_ARG;
-  if (H % 64 || F % 64 || E > 1024 || T > 16 || T * kk > 256 || kk > 32) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (H % 64 || F % 64 || F > kB16MaxF || E > 1024 || T > 16 || T * kk > 256 || kk > 32 ||
+      T * (2 * (int64_t)H + 64) > kB16MaxX)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
   if (!layer->gate_up || !layer->down || !x || (!wr && !logits) || !y) return MOE_ERR_INVALID_ARG;
   if ((idx == nullptr) != (w == nullptr)) return MOE_ERR_INVALID_ARG;
@@ -97,33 +633,29 @@ extern "C" MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer,
   for (const void *p : {(const void *)logits, (const void *)idx, (const void *)w})
     if (reinterpret_cast<uintptr_t>(p) % 4) return MOE_ERR_INVALID_ARG;
   if (!ws || ws_bytes < moe_decode_layer_bf16_workspace_bytes(T, k, shared, E, H, F)) return MOE_ERR_WORKSPACE;
-  uint8_t *base = static_cast<uint8_t *>(ws) + kB16CtrlBytes;
-  DecodeBf16Args a;
+  DecodeBf16Args a = {};
   a.gu = layer->gate_up;
   a.dn = layer->down;
   a.x = x;
   a.wr = wr;
   a.sg = shared_gate;
   a.residual = residual;
-  a.h = reinterpret_cast<float *>(base);
-  a.logits_ws = wr && logits ? logits : reinterpret_cast<float *>(base + sizeof(uint64_t) * (size_t)T * kk * F);
-  a.logits = wr ? a.logits_ws : logits;
+  a.logits = logits;
+  a.ctrl = static_cast<unsigned int *>(ws);
+  a.hbuf = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(ws) + kB16CtrlBytes);
+  a.lbuf = a.hbuf + (size_t)T * kk * F;
   a.y = y;
-  // routing outputs and the shared gate: in the control words when not asked for
-  a.idx = idx ? idx : static_cast<int32_t *>(ws);
-  a.w = w ? w : static_cast<float *>(ws) + 256;
-  a.sgate = static_cast<float *>(ws) + 512;
+  a.idx = idx;
+  a.w = w;
+  a.err = device_error_word();
+  if (!a.err) return MOE_ERR_CUDA;
   a.T = T;
-  a.k = k;
+  a.kk = kk;
   a.shared = shared;
   a.E = E;
   a.H = H;
   a.F = F;
   cudaStream_t s = as_stream(stream);
-  moe_status st = MOE_OK;
-  if (wr || shared_gate) st = launch_pdl(db16_logits_kernel, dim3(Er / 8 + 1, T), dim3(256), 0, s, a);
-  if (st == MOE_OK) st = route_rows(a.logits, T, Er, k, a.idx, a.w, s);
-  if (st == MOE_OK) st = launch_pdl(db16_h_kernel, dim3(F / 8, T * kk), dim3(256), 0, s, a);
-  if (st == MOE_OK) st = launch_pdl(db16_y_kernel, dim3(H / 8, T), dim3(256), 0, s, a);
-  return st;
+  if (T <= 8) return Er <= 256 ? decode_bf16_launch<8, 8>(a, s) : decode_bf16_launch<8, 32>(a, s);
+  return Er <= 256 ? decode_bf16_launch<16, 8>(a, s) : decode_bf16_launch<16, 32>(a, s);
 }

@@ -72,7 +72,8 @@ def decode(E=8, H=128, F=64, gu=P, dn=P, x=P, wr=P, logits=None, T=2, k=2, share
     (SHAPE, dict(H=96)), (SHAPE, dict(F=32)), (SHAPE, dict(T=17)), (SHAPE, dict(E=64, T=16, k=17)),
     (SHAPE, dict(E=1025)), (SHAPE, dict(E=64, T=1, k=33)), (SHAPE, dict(E=64, T=1, k=32, shared=1)),
     (SHAPE, dict(E=64, T=16, k=16, shared=1)),
-    (WS, dict(ws=None)), (WS, dict(ws_bytes=100)), (moe.MOE_OK, dict(T=0)),
+    (SHAPE, dict(T=16, H=5184)), (SHAPE, dict(T=1, H=83008)), (SHAPE, dict(F=(1 << 20) + 64)),
+    (WS, dict(ws=None)), (WS, dict(ws_bytes=100)), (WS, dict(T=16, H=5120, ws_bytes=100)), (moe.MOE_OK, dict(T=0)),
 ])
 def test_decode_layer_refusals(want, kw):
     assert decode(**kw) == want
