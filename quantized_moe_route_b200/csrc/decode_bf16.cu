@@ -5,10 +5,11 @@
 //
 // A decode step reads each selected expert's weights once (6 H F bytes) and
 // does little else, so the kernel is a stream: a persistent grid, one CTA per
-// SM, whose producer warp copies weight rows as they lie in memory
-// (cp.async.bulk, one row piece a lane) through a ring of ~17 KB stages, and
-// 16 consumer warps that each take whole units of work from it, so no barrier
-// between warps sits on the stream.
+// SM, whose producer thread brings weight tiles by TMA through a ring of 16 KB
+// stages, and 16 consumer warps that each take whole units of work from it, so
+// no barrier between warps sits on the stream.  (One TMA box per 16 KB streams
+// 7.1 TB/s over 148 CTAs with nothing else to do; the same bytes as 16 row
+// copies of 1 KB reach 2.8 TB/s, as four of 4 KB 4.5 TB/s.)
 //   phase A  unit = 4 or 8 features of one expert (their gate and up rows, all
 //            H inputs).  Units go round the CTAs; h is published as 8-byte
 //            words {fp32 h, call epoch} (single-copy atomic: a reader polls
@@ -20,11 +21,13 @@
 //            do not depend on h and are loaded while h is still on its way.
 // Dot products run on m16n8k16 tensor-core instructions with the weight rows
 // as A and the tokens as B.  A sum over k may take k in any order, so lane
-// (g, t) reads 16 consecutive bytes of its row per 32 inputs and uses them as
-// the fragments of two instructions; rows are 64 bytes (mod 128) apart in
-// shared memory, so eight lanes' 16-byte reads touch every bank once.  The
-// down projection takes h as a pair of bf16 values (hi + lo, 16 significant
-// bits): the second product is free in a kernel bound by its stream.
+// (g, t) reads the 16-byte pieces 2t and 2t + 1 of its row's 64 inputs and uses
+// each as the fragments of two instructions.  Weight rows arrive in the
+// 128-byte swizzle (piece p of row r at p ^ (r mod 8)) and token rows lie 16
+// bytes (mod 128) apart, so in both the eight lanes of a 16-byte read touch
+// every bank once.  The down projection takes h as a pair of bf16 values (hi +
+// lo, 16 significant bits): the second product is free in a kernel bound by its
+// stream.
 //
 // The router's logits are computed over the grid (each CTA its experts' rows,
 // K split over the warps, partial sums added in warp order), published as
@@ -35,6 +38,7 @@
 #include "decode_common.cuh"
 #include "decode_items.cuh"
 #include "route.cuh"
+#include "tcgen05.cuh"
 #include "w16.cuh"
 
 namespace moe {
@@ -42,7 +46,7 @@ namespace moe {
 constexpr int kB16Warps = 16;                         // consumers; one more warp produces
 constexpr int kB16Threads = (kB16Warps + 1) * 32;
 constexpr int kB16KC = 512;                           // inputs of a 16-row stage (an 8-row stage: twice that)
-constexpr uint32_t kB16Stage = 16 * (kB16KC * 2 + 64);  // bytes of a stage
+constexpr uint32_t kB16Stage = 16 * kB16KC * 2;       // bytes of a stage
 constexpr int kB16MaxStages = 12;
 constexpr int kB16MaxF = 1 << 20;
 constexpr int kB16MaxX = 166000;                      // bytes of x rows that fit beside two stages
@@ -62,6 +66,7 @@ struct DecodeBf16Args {
   int *err;
   int T, kk, shared, E, H, F;  // kk: rows per token (k + shared)
   int nst;                     // ring stages
+  int R;                       // output channels of a phase B strip (at most 16)
   uint32_t hb_bytes;           // per-warp h buffer
 };
 
@@ -69,15 +74,15 @@ struct B16Smem {
   uint32_t x, rows, tables, total;  // byte offsets; the ring is at 0
 };
 __host__ __device__ inline uint32_t b16_hb_bytes(int T) {  // one token's (two tokens') 512 h values as hi + lo, or 8 x 64
-  return T == 1 ? 2176u : 4352u;
+  return T == 1 ? 2080u : 4160u;
 }
 __host__ __device__ inline B16Smem b16_layout(int T, int kk, int H, int nst) {
   B16Smem L;
   L.x = (uint32_t)nst * kB16Stage;
-  const uint32_t xb = (uint32_t)T * (uint32_t)(H * 2 + 64), hb = kB16Warps * b16_hb_bytes(T);
+  const uint32_t xb = (uint32_t)T * (uint32_t)(H * 2 + 16), hb = kB16Warps * b16_hb_bytes(T);
   L.rows = L.x + (xb > hb ? xb : hb);  // x in phase A, the warps' h in phase B
   L.tables = L.rows + (uint32_t)(T * kk) * 64u;
-  L.total = L.tables + 32 * 4 + 256 * 4 + 256 * 16 + 256 * 4 + 256 * 4 + 256 * 4 + 2 * 8 * kB16MaxStages + 64;
+  L.total = L.tables + 32 * 4 + 256 * 4 + 256 * 16 + 256 * 4 + 256 * 4 + 256 * 4 + 2 * 8 * kB16MaxStages + 64 + 1024 /* alignment of the ring */;
   return L;
 }
 
@@ -97,12 +102,14 @@ __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
 // kRows: weight rows of a phase A unit, half gate and half up (8: up to 8
 // tokens; 16: two token columns of 8).  PER: logits per lane in the routing.
 template <int kRows, int PER>
-__global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16Args a) {
+__global__ void __launch_bounds__(kB16Threads, 1)
+    decode_bf16_kernel(DecodeBf16Args a, const __grid_constant__ CUtensorMap gu_map,
+                       const __grid_constant__ CUtensorMap dn_map) {
   constexpr int NB = kRows == 16 ? 2 : 1;        // token blocks of 8
   constexpr int FPU = kRows / 2;                 // features of a unit
   constexpr int KCA = kRows == 16 ? kB16KC : 2 * kB16KC;
-  constexpr uint32_t pitchA = KCA * 2 + 64, pitchB = kB16KC * 2 + 64;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const B16Smem L = b16_layout(a.T, a.kk, a.H, a.nst);
   float *rowbuf = reinterpret_cast<float *>(smem + L.rows);            // [T kk][16]
   uint32_t *emask = reinterpret_cast<uint32_t *>(smem + L.tables);     // [32] expert presence bits
@@ -117,7 +124,7 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int T = a.T, kk = a.kk, H = a.H, F = a.F, Er = a.E - a.shared, G = gridDim.x, nst = a.nst;
-  const uint32_t xpitch = (uint32_t)(H * 2 + 64);
+  const uint32_t xpitch = (uint32_t)(H * 2 + 16);
 
   if (tid == 0) {
     for (int s = 0; s < nst; ++s) {
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
   const int myUnits = (int)blockIdx.x < nUnits ? (nUnits - 1 - (int)blockIdx.x) / G + 1 : 0;
   const int CA = (H + KCA - 1) / KCA, CB = (F + kB16KC - 1) / kB16KC;
   const int nA = myUnits * CA;  // stages of phase A
-  const int per_cta = (H + 16 * G - 1) / (16 * G), R = (H + per_cta * G - 1) / (per_cta * G);
+  const int R = a.R;
   const int nStrips = (H + R - 1) / R;
   const int myStrips = (int)blockIdx.x < nStrips ? (nStrips - 1 - (int)blockIdx.x) / G + 1 : 0;
 
@@ -316,34 +323,33 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
       }
     }
     __syncwarp();
-    const uint64_t pol = policy_evict_first();
     int ord = 0;
-    bool ok = true;
-    // one row piece per lane: nrows rows of `bytes` bytes, src this lane's row
-    auto put = [&](const uint16_t *src, int nrows, uint32_t bytes, uint32_t pitch) {
-      const int s = ord % nst;
-      if (!__all_sync(0xffffffffu, wait_bar(&empty[s], ((ord / nst) & 1) ^ 1))) return false;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[s], bytes * (uint32_t)nrows);
-        misc[2] = ord + 1;
+    if (lane == 0) {
+      bool ok = true;
+      // the stage of use `ord`, free and armed for `bytes`
+      auto arm = [&](uint32_t bytes) {
+        const int s = ord % nst;
+        if (!wait_bar(&empty[s], ((ord / nst) & 1) ^ 1)) return false;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        misc[2] = ++ord;
+        return true;
+      };
+      for (int q = 0; q < myUnits && ok; ++q) {
+        const int unit = blockIdx.x + q * G, slot = unit / UA, f0 = (unit - slot * UA) * FPU, e = slot_expert[slot];
+        for (int c = 0; c < CA && (ok = arm(kB16Stage)); ++c) {
+          const int s = (ord - 1) % nst;
+          tma_load_5d(smem + (size_t)s * kB16Stage, &gu_map, 0, f0, 0, c * (KCA / 64), e, &full[s]);
+        }
       }
-      __syncwarp();
-      if (lane < nrows) bulk_g2s_evict_first(smem + (size_t)s * kB16Stage + lane * pitch, src, bytes, &full[s], pol);
-      ++ord;
-      return true;
-    };
-    for (int q = 0; q < myUnits && ok; ++q) {
-      const int unit = blockIdx.x + q * G, slot = unit / UA, f0 = (unit - slot * UA) * FPU;
-      const int row = lane < FPU ? f0 + lane : F + f0 + (lane & (FPU - 1));
-      const uint16_t *src = a.gu + ((size_t)slot_expert[slot] * 2 * F + row) * H;
-      for (int c = 0; c < CA && ok; ++c) ok = put(src + c * KCA, kRows, 2u * (uint32_t)min(KCA, H - c * KCA), pitchA);
-    }
-    for (int si = 0; si < myStrips && ok; ++si) {
-      const int row0 = (blockIdx.x + si * G) * R, nr = min(R, H - row0);
-      for (int u = 0; u < U && ok; ++u) {
-        const uint16_t *src = a.dn + ((size_t)slot_expert[u] * H + row0 + min(lane, nr - 1)) * F;
-        for (int c = 0; c < CB && ok; ++c)
-          ok = put(src + c * kB16KC, nr, 2u * (uint32_t)min(kB16KC, F - c * kB16KC), pitchB);
+      for (int si = 0; si < myStrips && ok; ++si) {
+        const int row0 = (blockIdx.x + si * G) * R;
+        for (int u = 0; u < U && ok; ++u) {
+          const int e = slot_expert[u];
+          for (int c = 0; c < CB && (ok = arm((uint32_t)R * (kB16KC * 2))); ++c) {
+            const int s = (ord - 1) % nst;
+            tma_load_4d(smem + (size_t)s * kB16Stage, &dn_map, 0, row0, c * (kB16KC / 64), e, &full[s]);
+          }
+        }
       }
     }
     // the last copies issued into each stage land before the CTA leaves, also
@@ -364,6 +370,8 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
     bool ok = true;
     // ---- phase A
     const uint32_t ring = smem_u32(smem), xs = smem_u32(smem + L.x);
+    // this lane's pieces 2 t and 2 t + 1 of row g (or g + 8) of a swizzled 8-row group
+    const uint32_t wo[2] = {(uint32_t)(g * 128 + (((2 * t4) ^ g) << 4)), (uint32_t)(g * 128 + (((2 * t4 + 1) ^ g) << 4))};
     for (int q = warp; q < myUnits && ok; q += kB16Warps) {
       const int unit = blockIdx.x + q * G, slot = unit / UA, f0 = (unit - slot * UA) * FPU;
       const uint32_t mask = tokmask[slot];
@@ -372,7 +380,7 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int n = nb * 8 + g;
-        xa[nb] = xs + (uint32_t)nth_bit(mask, n < ntok ? n : 0) * xpitch + 16u * t4;
+        xa[nb] = xs + (uint32_t)nth_bit(mask, n < ntok ? n : 0) * xpitch + 32u * t4;
       }
       const bool two = NB == 2 && ntok > 8;
       float acc[NB][2][4] = {};
@@ -382,20 +390,23 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
           ok = false;
           break;
         }
-        const uint32_t wa = ring + (uint32_t)s * kB16Stage + (uint32_t)g * pitchA + 16u * t4;
-        const int nblk = min(KCA, H - c * KCA) / 32;
-        const uint32_t xo = (uint32_t)(c * KCA * 2);
+        uint32_t wa = ring + (uint32_t)s * kB16Stage;
+        const int nch = min(KCA, H - c * KCA) / 64;
+        uint32_t xo = (uint32_t)(c * KCA * 2);
 #pragma unroll 4
-        for (int b = 0; b < nblk; ++b) {
-          const uint4 w0 = lds_u4(wa + 64 * b);
-          const uint4 w1 = kRows == 16 ? lds_u4(wa + 8 * pitchA + 64 * b) : make_uint4(0, 0, 0, 0);
-          const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+        for (int b = 0; b < nch; ++b, wa += kRows * 128, xo += 128) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            if (nb == 1 && !two) continue;
-            const uint4 v = lds_u4(xa[nb] + xo + 64 * b);
-            mma_bf16_16816(acc[nb][0], f0r, v.x, v.y);
-            mma_bf16_16816(acc[nb][1], f1r, v.z, v.w);
+          for (int i = 0; i < 2; ++i) {
+            const uint4 w0 = lds_u4(wa + wo[i]);
+            const uint4 w1 = kRows == 16 ? lds_u4(wa + 1024 + wo[i]) : make_uint4(0, 0, 0, 0);
+            const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              if (nb == 1 && !two) continue;
+              const uint4 v = lds_u4(xa[nb] + xo + 16 * i);
+              mma_bf16_16816(acc[nb][0], f0r, v.x, v.y);
+              mma_bf16_16816(acc[nb][1], f1r, v.z, v.w);
+            }
           }
         }
         __syncwarp();
@@ -438,17 +449,17 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
         float acc[2][2][4] = {};
         for (int c = 0; c < CB && ok; ++c) {
           const int o = nA + (J + u) * CB + c, s = o % nst, cc = min(kB16KC, F - c * kB16KC);
-          const uint32_t wa = ring + (uint32_t)s * kB16Stage + (uint32_t)g * pitchB + 16u * t4;
+          const uint32_t wa = ring + (uint32_t)s * kB16Stage;
           bool landed = false;
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb) {
             if (8 * nb >= ntok) break;
             const int m = min(8, ntok - 8 * nb);  // tokens of this block
             int fc = kB16KC;                      // inputs whose h fits the warp's buffer
-            while ((uint32_t)(m * (fc * 2 + 64) * 2) > a.hb_bytes) fc >>= 1;
+            while ((uint32_t)(m * (fc * 2 + 16) * 2) > a.hb_bytes) fc >>= 1;
             for (int k1 = 0; k1 < cc && ok; k1 += fc) {
               const int kc = min(fc, cc - k1), per = kc / 64;  // 16-byte word pairs of a token per lane
-              const uint32_t hp = (uint32_t)(kc * 2 + 64);     // bytes between tokens
+              const uint32_t hp = (uint32_t)(kc * 2 + 16);     // bytes between tokens
               const uint32_t lo_off = (uint32_t)m * hp;
               __syncwarp();
               for (int i0 = 0; i0 < m * per && ok; i0 += 8) {
@@ -497,17 +508,21 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
                 landed = true;
               }
               if (!ok) break;
-              const uint32_t ha = hb + (uint32_t)min(g, m - 1) * hp + 16u * t4;
-              const uint32_t wk = wa + (uint32_t)k1 * 2u;
+              uint32_t ha = hb + (uint32_t)min(g, m - 1) * hp + 32u * t4;
+              int line = (k1 / 64) * R + g;  // 128-byte line of row g; its swizzle is the line's place among eight
 #pragma unroll 4
-              for (int b = 0; b < kc / 32; ++b) {
-                const uint4 w0 = lds_u4(wk + 64 * b), w1 = lds_u4(wk + 8 * pitchB + 64 * b);
-                const uint4 vh = lds_u4(ha + 64 * b), vl = lds_u4(ha + lo_off + 64 * b);
-                const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
-                mma_bf16_16816(acc[nb][0], f0r, vh.x, vh.y);
-                mma_bf16_16816(acc[nb][1], f1r, vh.z, vh.w);
-                mma_bf16_16816(acc[nb][0], f0r, vl.x, vl.y);
-                mma_bf16_16816(acc[nb][1], f1r, vl.z, vl.w);
+              for (int b = 0; b < kc / 64; ++b, line += R, ha += 128) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t wk = wa + (uint32_t)(line * 128 + (((2 * t4 + i) ^ (line & 7)) << 4));
+                  const uint4 w0 = lds_u4(wk), w1 = lds_u4(wk + 1024);
+                  const uint4 vh = lds_u4(ha + 16 * i), vl = lds_u4(ha + lo_off + 16 * i);
+                  const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+                  mma_bf16_16816(acc[nb][0], f0r, vh.x, vh.y);
+                  mma_bf16_16816(acc[nb][1], f1r, vh.z, vh.w);
+                  mma_bf16_16816(acc[nb][0], f0r, vl.x, vl.y);
+                  mma_bf16_16816(acc[nb][1], f1r, vl.z, vl.w);
+                }
               }
             }
           }
@@ -554,6 +569,26 @@ __global__ void __launch_bounds__(kB16Threads, 1) decode_bf16_kernel(DecodeBf16A
   }
 }
 
+// gate_up [E][2][F][H] as 64-input columns: box = 64 inputs x kRows / 2
+// features x {gate, up} x the stage's columns; down [E][H][F]: box = 64 inputs
+// x R outputs x 8 columns.  128-byte swizzle, zeros outside.
+static bool b16_maps(CUtensorMap *gu, CUtensorMap *dn, const DecodeBf16Args &a, int rows) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t E = a.E, H = a.H, F = a.F;
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const cuuint64_t d1[5] = {64, F, 2, H / 64, E}, s1[4] = {H * 2, F * H * 2, 128, 2 * F * H * 2};
+  const cuuint32_t b1[5] = {64, (cuuint32_t)rows / 2, 2, (cuuint32_t)(kB16Stage / 128 / rows), 1};
+  const cuuint64_t d2[4] = {64, H, F / 64, E}, s2[3] = {F * 2, 128, H * F * 2};
+  const cuuint32_t b2[4] = {64, (cuuint32_t)a.R, kB16KC / 64, 1};
+  return fn(gu, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<uint16_t *>(a.gu), d1, s1, b1, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+         fn(dn, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t *>(a.dn), d2, s2, b2, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kRows, int PER>
 static moe_status decode_bf16_launch(DecodeBf16Args &a, cudaStream_t stream) {
   auto kern = decode_bf16_kernel<kRows, PER>;
@@ -583,8 +618,16 @@ static moe_status decode_bf16_launch(DecodeBf16Args &a, cudaStream_t stream) {
     if (occ < 1) return MOE_ERR_UNSUPPORTED_SHAPE;
     per_sm[dev].store(occ, std::memory_order_release);
   }
+  // phase B strips: equal shares of the outputs, at most 16 a strip
+  const int G = sms * per_sm[dev].load(std::memory_order_acquire), per_cta = (a.H + 16 * G - 1) / (16 * G);
+  a.R = (a.H + per_cta * G - 1) / (per_cta * G);
+  CUtensorMap gu_map, dn_map;
+  if (!b16_maps(&gu_map, &dn_map, a, kRows)) {
+    set_cuda_error(cudaErrorInvalidValue);
+    return MOE_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(sms * per_sm[dev].load(std::memory_order_acquire));
+  cfg.gridDim = dim3(G);
   cfg.blockDim = dim3(kB16Threads);
   cfg.dynamicSmemBytes = L.total;
   cfg.stream = stream;
@@ -595,7 +638,7 @@ static moe_status decode_bf16_launch(DecodeBf16Args &a, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, gu_map, dn_map);
   if (e != cudaSuccess) {
     set_cuda_error(e);
     return MOE_ERR_CUDA;
