@@ -6,16 +6,18 @@
 // A decode step reads each selected expert's weights once (6 H F bytes) and
 // does little else, so the kernel is a stream: a persistent grid, one CTA per
 // SM, whose producer thread brings weight tiles by TMA through a ring of 16 KB
-// stages, and 16 consumer warps that each take whole units of work from it, so
+// stages, and 15 consumer warps that each take whole units of work from it, so
 // no barrier between warps sits on the stream.  (One TMA box per 16 KB streams
 // 7.1 TB/s over 148 CTAs with nothing else to do; the same bytes as 16 row
 // copies of 1 KB reach 2.8 TB/s, as four of 4 KB 4.5 TB/s.)
 //   phase A  unit = 4 or 8 features of one expert (their gate and up rows, all
 //            H inputs).  Units go round the CTAs; h is published as 8-byte
-//            words {fp32 h, call epoch} (single-copy atomic: a reader polls
-//            the words themselves, no fence or counter on the path).
+//            words {h as a bf16 pair, call epoch} (single-copy atomic: a
+//            reader polls the words themselves, no fence or counter on the
+//            path).
 //   phase B  a CTA owns R output channels (H / CTAs, at most 16) and runs
-//            every selected expert's rows of them, one warp per expert: all k
+//            every selected expert's rows of them, one warp per expert and four
+//            tokens (a busier expert's tile is loaded again, from L2): all k
 //            rows of a token meet in the CTA's shared memory, so the combine
 //            needs no second handoff.  The producer runs ahead: these weights
 //            do not depend on h and are loaded while h is still on its way.
@@ -43,11 +45,13 @@
 
 namespace moe {
 
-constexpr int kB16Warps = 16;                         // consumers; one more warp produces
-constexpr int kB16Threads = (kB16Warps + 1) * 32;
+constexpr int kB16All = 16;                           // warps: 15 consumers and the producer
+constexpr int kB16Warps = kB16All - 1;                // (a 17th warp would cost every thread 32 registers)
+constexpr int kB16Threads = kB16All * 32;
 constexpr int kB16KC = 512;                           // inputs of a 16-row stage (an 8-row stage: twice that)
 constexpr uint32_t kB16Stage = 16 * kB16KC * 2;       // bytes of a stage
-constexpr int kB16MaxStages = 12;
+constexpr int kB16MaxStages = 8;                      // a power of two, like every smaller ring
+constexpr int kB16JobTok = 4;                         // tokens of a phase B job
 constexpr int kB16MaxF = 1 << 20;
 constexpr int kB16MaxX = 166000;                      // bytes of x rows that fit beside two stages
 constexpr size_t kB16CtrlBytes = 4096;                // workspace head: epoch, done counter
@@ -57,7 +61,7 @@ constexpr uint32_t kB16BarPolls = 1u << 19;           // bound of a barrier wait
 struct DecodeBf16Args {
   const uint16_t *gu, *dn, *x, *wr, *sg, *residual;
   float *logits;             // [T][Er]: the input, or with wr an optional output
-  unsigned long long *hbuf;  // [T kk][F] words {fp32 h, epoch}
+  unsigned long long *hbuf;  // [T kk][F] words {bf16 lo, bf16 hi, epoch}: h = hi + lo
   unsigned long long *lbuf;  // [T][Er + 1] words {fp32 logit, epoch}; entry Er: the shared expert's gate
   unsigned int *ctrl;        // [0] last epoch, [1] CTAs done
   uint16_t *y;
@@ -65,7 +69,7 @@ struct DecodeBf16Args {
   float *w;
   int *err;
   int T, kk, shared, E, H, F;  // kk: rows per token (k + shared)
-  int nst;                     // ring stages
+  int nst_log2;                // ring stages
   int R;                       // output channels of a phase B strip (at most 16)
   uint32_t hb_bytes;           // per-warp h buffer
 };
@@ -73,8 +77,8 @@ struct DecodeBf16Args {
 struct B16Smem {
   uint32_t x, rows, tables, total;  // byte offsets; the ring is at 0
 };
-__host__ __device__ inline uint32_t b16_hb_bytes(int T) {  // one token's (two tokens') 512 h values as hi + lo, or 8 x 64
-  return T == 1 ? 2080u : 4160u;
+__host__ __device__ inline uint32_t b16_hb_bytes(int T) {  // 512 h values (hi and lo) of a token or two, 256 of four
+  return T == 1 ? 2080u : 4224u;
 }
 __host__ __device__ inline B16Smem b16_layout(int T, int kk, int H, int nst) {
   B16Smem L;
@@ -82,11 +86,11 @@ __host__ __device__ inline B16Smem b16_layout(int T, int kk, int H, int nst) {
   const uint32_t xb = (uint32_t)T * (uint32_t)(H * 2 + 16), hb = kB16Warps * b16_hb_bytes(T);
   L.rows = L.x + (xb > hb ? xb : hb);  // x in phase A, the warps' h in phase B
   L.tables = L.rows + (uint32_t)(T * kk) * 64u;
-  L.total = L.tables + 32 * 4 + 256 * 4 + 256 * 16 + 256 * 4 + 256 * 4 + 256 * 4 + 2 * 8 * kB16MaxStages + 64 + 1024 /* alignment of the ring */;
+  L.total = L.tables + 32 * 4 + 256 * 4 + 256 * 16 + 256 * 4 + 256 * 4 + 256 * 4 + 320 * 2 + 2 * 8 * kB16MaxStages + 64 + 1024 /* alignment of the ring */;
   return L;
 }
 
-__device__ __forceinline__ void b16_consumer_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void b16_consumer_sync() { asm volatile("bar.sync 1, 480;" ::: "memory"); }
 __device__ __forceinline__ void st_relaxed_u64(unsigned long long *p, unsigned long long v) {
   asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
@@ -110,7 +114,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
   constexpr int KCA = kRows == 16 ? kB16KC : 2 * kB16KC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const B16Smem L = b16_layout(a.T, a.kk, a.H, a.nst);
+  const B16Smem L = b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2);
   float *rowbuf = reinterpret_cast<float *>(smem + L.rows);            // [T kk][16]
   uint32_t *emask = reinterpret_cast<uint32_t *>(smem + L.tables);     // [32] expert presence bits
   uint32_t *tokmask = emask + 32;                                      // [256] tokens of a slot
@@ -118,12 +122,13 @@ __global__ void __launch_bounds__(kB16Threads, 1)
   int *slot_expert = reinterpret_cast<int *>(slot_j + 256 * 16);       // [256]
   int *ridx = slot_expert + 256;                                       // [256] expert of a row
   float *rw = reinterpret_cast<float *>(ridx + 256);                   // [256] weight of a row
-  uint64_t *full = reinterpret_cast<uint64_t *>(rw + 256);
+  uint16_t *jobs = reinterpret_cast<uint16_t *>(rw + 256);             // [320] phase B: slot + 256 * group of tokens
+  uint64_t *full = reinterpret_cast<uint64_t *>(jobs + 320);
   uint64_t *empty = full + kB16MaxStages;
-  volatile int *misc = reinterpret_cast<volatile int *>(empty + kB16MaxStages);  // [0] abort, [1] epoch, [2] stages issued
+  volatile int *misc = reinterpret_cast<volatile int *>(empty + kB16MaxStages);  // [0] abort, [1] epoch, [2] stages issued, [3] jobs listed, [4] jobs
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int T = a.T, kk = a.kk, H = a.H, F = a.F, Er = a.E - a.shared, G = gridDim.x, nst = a.nst;
+  const int T = a.T, kk = a.kk, H = a.H, F = a.F, Er = a.E - a.shared, G = gridDim.x, nst = 1 << a.nst_log2;
   const uint32_t xpitch = (uint32_t)(H * 2 + 16);
 
   if (tid == 0) {
@@ -133,6 +138,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
     }
     misc[0] = 0;
     misc[2] = 0;
+    misc[3] = 0;
     fence_mbar_init();
   }
   if (tid < 32) emask[tid] = 0u;
@@ -142,13 +148,11 @@ __global__ void __launch_bounds__(kB16Threads, 1)
     const unsigned int ep = a.ctrl[0] + 1u;  // this call's epoch; never 0 (zeroed words never match)
     misc[1] = (int)(ep == 0u ? 1u : ep);
   }
-  if (warp < kB16Warps) {
-    for (int v = tid; v < T * (H / 8); v += kB16Warps * 32) {
-      const int t = v / (H / 8), c = v - t * (H / 8);
-      cp_async_16(smem + L.x + (size_t)t * xpitch + 16 * c, a.x + (size_t)t * H + 8 * c);
-    }
-    cp_async_commit();
+  for (int v = tid; v < T * (H / 8); v += kB16Threads) {
+    const int t = v / (H / 8), c = v - t * (H / 8);
+    cp_async_16(smem + L.x + (size_t)t * xpitch + 16 * c, a.x + (size_t)t * H + 8 * c);
   }
+  cp_async_commit();
   auto fail = [&](int code) {
     atomicExch(a.err, code);
     misc[0] = 1;
@@ -167,7 +171,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
       float d[2][4] = {};
       const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
-      for (int b = warp; b < H / 32 && warp < kB16Warps; b += kB16Warps) {
+      for (int b = warp; b < H / 32; b += kB16All) {
         const int c = 32 * b + 8 * t4;
         const uint4 w0 = r0 ? *reinterpret_cast<const uint4 *>(r0 + c) : z;
         const uint4 w1 = r1 ? *reinterpret_cast<const uint4 *>(r1 + c) : z;
@@ -181,16 +185,14 @@ __global__ void __launch_bounds__(kB16Threads, 1)
           mma_bf16_16816(d[1], f1, q1.z, q1.w);
         }
       }
-      if (warp < kB16Warps) {
-        float *p = part + warp * 256;
+      float *p = part + warp * 256;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int n = nb * 8 + 2 * t4;
-          p[g * 16 + n] = d[nb][0];
-          p[g * 16 + n + 1] = d[nb][1];
-          p[(g + 8) * 16 + n] = d[nb][2];
-          p[(g + 8) * 16 + n + 1] = d[nb][3];
-        }
+      for (int nb = 0; nb < NB; ++nb) {
+        const int n = nb * 8 + 2 * t4;
+        p[g * 16 + n] = d[nb][0];
+        p[g * 16 + n + 1] = d[nb][1];
+        p[(g + 8) * 16 + n] = d[nb][2];
+        p[(g + 8) * 16 + n + 1] = d[nb][3];
       }
       __syncthreads();
       if (tid < 256) {
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         if (t < T && e < hi) {
           float v = 0.f;
 #pragma unroll
-          for (int w = 0; w < kB16Warps; ++w) v += part[w * 256 + tid];
+          for (int w = 0; w < kB16All; ++w) v += part[w * 256 + tid];
           st_relaxed_u64(a.lbuf + (size_t)t * (Er + 1) + e,
                          ((unsigned long long)__float_as_uint(v) << 32) | (unsigned int)misc[1]);
           if (e < Er && a.logits) a.logits[(size_t)t * Er + e] = v;
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
       }
       __nanosleep(32);
     }
-    return wait_bar(&full[ord % nst], (ord / nst) & 1);
+    return wait_bar(&full[ord & (nst - 1)], (ord >> a.nst_log2) & 1);
   };
 
   if (warp == kB16Warps) {
@@ -325,11 +327,12 @@ __global__ void __launch_bounds__(kB16Threads, 1)
     __syncwarp();
     int ord = 0;
     if (lane == 0) {
+      const uint64_t pol = policy_evict_first();
       bool ok = true;
       // the stage of use `ord`, free and armed for `bytes`
       auto arm = [&](uint32_t bytes) {
-        const int s = ord % nst;
-        if (!wait_bar(&empty[s], ((ord / nst) & 1) ^ 1)) return false;
+        const int s = ord & (nst - 1);
+        if (!wait_bar(&empty[s], ((ord >> a.nst_log2) & 1) ^ 1)) return false;
         mbar_arrive_expect_tx(&full[s], bytes);
         misc[2] = ++ord;
         return true;
@@ -337,17 +340,27 @@ __global__ void __launch_bounds__(kB16Threads, 1)
       for (int q = 0; q < myUnits && ok; ++q) {
         const int unit = blockIdx.x + q * G, slot = unit / UA, f0 = (unit - slot * UA) * FPU, e = slot_expert[slot];
         for (int c = 0; c < CA && (ok = arm(kB16Stage)); ++c) {
-          const int s = (ord - 1) % nst;
-          tma_load_5d(smem + (size_t)s * kB16Stage, &gu_map, 0, f0, 0, c * (KCA / 64), e, &full[s]);
+          const int s = (ord - 1) & (nst - 1);
+          tma_load_5d_hint(smem + (size_t)s * kB16Stage, &gu_map, 0, f0, 0, c * (KCA / 64), e, &full[s], pol);
         }
+      }
+      int nJobs = U;
+      if (ok && myStrips && T > kB16JobTok) {
+        for (uint32_t i = 0; !misc[3] && ok; ++i) {
+          if (i > kB16Polls) fail(DEVERR_DECODE_H_WAIT);
+          ok = !misc[0];
+          __nanosleep(32);
+        }
+        __threadfence_block();
+        nJobs = misc[4];
       }
       for (int si = 0; si < myStrips && ok; ++si) {
         const int row0 = (blockIdx.x + si * G) * R;
-        for (int u = 0; u < U && ok; ++u) {
-          const int e = slot_expert[u];
+        for (int j = 0; j < nJobs && ok; ++j) {
+          const int e = slot_expert[T > kB16JobTok ? jobs[j] & 255 : j];
           for (int c = 0; c < CB && (ok = arm((uint32_t)R * (kB16KC * 2))); ++c) {
-            const int s = (ord - 1) % nst;
-            tma_load_4d(smem + (size_t)s * kB16Stage, &dn_map, 0, row0, c * (kB16KC / 64), e, &full[s]);
+            const int s = (ord - 1) & (nst - 1);
+            tma_load_4d_hint(smem + (size_t)s * kB16Stage, &dn_map, 0, row0, c * (kB16KC / 64), e, &full[s], pol);
           }
         }
       }
@@ -355,18 +368,34 @@ __global__ void __launch_bounds__(kB16Threads, 1)
     // the last copies issued into each stage land before the CTA leaves, also
     // when the consumers gave up
     if (lane == 0)
-      for (int o = max(0, ord - nst); o < ord; ++o) mbar_wait_bounded(&full[o % nst], (o / nst) & 1, 1u << 20);
+      for (int o = max(0, ord - nst); o < ord; ++o) mbar_wait_bounded(&full[o & (nst - 1)], (o >> a.nst_log2) & 1, 1u << 20);
   } else {
     // ------------------------------------------------------------ consumers
-    if (tid < T * kk) {
-      const int t = tid / kk, e = ridx[tid];
-      int slot = 0;  // rank of e among the selected
-      for (int w = 0; w < (e >> 5); ++w) slot += __popc(emask[w]);
-      slot += __popc(emask[e >> 5] & ((1u << (e & 31)) - 1u));
-      atomicOr(&tokmask[slot], 1u << t);
-      slot_j[slot * 16 + t] = (uint8_t)(tid - t * kk);
+    if (warp * 32 < T * kk) {
+      const int r = min(tid, T * kk - 1), t = r / kk, e = ridx[r];
+      const int below = __shfl_sync(0xffffffffu, ebase, e >> 5);
+      const uint32_t word = __shfl_sync(0xffffffffu, em, e >> 5);
+      const int slot = below + __popc(word & ((1u << (e & 31)) - 1u));
+      if (tid < T * kk) {
+        atomicOr(&tokmask[slot], 1u << t);
+        slot_j[slot * 16 + t] = (uint8_t)(r - t * kk);
+      }
     }
     b16_consumer_sync();
+    if (T > kB16JobTok && warp == kB16Warps - 1) {  // the jobs of phase B; eight slots a lane
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += (__popc(tokmask[8 * lane + i]) + kB16JobTok - 1) / kB16JobTok;
+      const int end = warp_inclusive_scan(n);
+      int at = end - n;
+      for (int i = 0; i < 8; ++i)
+        for (int sub = 0; sub * kB16JobTok < __popc(tokmask[8 * lane + i]); ++sub)
+          jobs[at++] = (uint16_t)(8 * lane + i + 256 * sub);
+      if (lane == 31) misc[4] = end;
+      __threadfence_block();
+      __syncwarp();
+      if (lane == 0) misc[3] = 1;  // for the producer; the consumers meet at the barrier after phase A
+    }
     bool ok = true;
     // ---- phase A
     const uint32_t ring = smem_u32(smem), xs = smem_u32(smem + L.x);
@@ -383,9 +412,9 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         xa[nb] = xs + (uint32_t)nth_bit(mask, n < ntok ? n : 0) * xpitch + 32u * t4;
       }
       const bool two = NB == 2 && ntok > 8;
-      float acc[NB][2][4] = {};
+      float acc[NB][4][4] = {};  // four independent chains
       for (int c = 0; c < CA; ++c) {
-        const int o = q * CA + c, s = o % nst;
+        const int o = q * CA + c, s = o & (nst - 1);
         if (!__all_sync(0xffffffffu, wait_full(o))) {
           ok = false;
           break;
@@ -404,8 +433,8 @@ __global__ void __launch_bounds__(kB16Threads, 1)
             for (int nb = 0; nb < NB; ++nb) {
               if (nb == 1 && !two) continue;
               const uint4 v = lds_u4(xa[nb] + xo + 16 * i);
-              mma_bf16_16816(acc[nb][0], f0r, v.x, v.y);
-              mma_bf16_16816(acc[nb][1], f1r, v.z, v.w);
+              mma_bf16_16816(acc[nb][2 * i], f0r, v.x, v.y);
+              mma_bf16_16816(acc[nb][2 * i + 1], f1r, v.z, v.w);
             }
           }
         }
@@ -417,7 +446,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
       for (int nb = 0; nb < NB; ++nb) {
         float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = acc[nb][0][i] + acc[nb][1][i];
+        for (int i = 0; i < 4; ++i) v[i] = (acc[nb][0][i] + acc[nb][1][i]) + (acc[nb][2][i] + acc[nb][3][i]);
         if (kRows == 8) {  // rows 0-3 gate, 4-7 up: the partner is 16 lanes up
           v[2] = __shfl_down_sync(0xffffffffu, v[0], 16);
           v[3] = __shfl_down_sync(0xffffffffu, v[1], 16);
@@ -429,8 +458,9 @@ __global__ void __launch_bounds__(kB16Threads, 1)
           if (n < ntok) {
             const int t = nth_bit(mask, n);
             const float h = activate(v[i], MOE_ACT_SILU) * v[2 + i];
+            const float hi = bf16_bits_to_f32(f32_to_bf16_bits(h));
             st_relaxed_u64(a.hbuf + (size_t)(t * kk + slot_j[slot * 16 + t]) * F + f0 + g,
-                           ((unsigned long long)__float_as_uint(h) << 32) | epoch);
+                           ((unsigned long long)cvt_bf16x2(hi, h - hi) << 32) | epoch);
           }
         }
       }
@@ -439,109 +469,111 @@ __global__ void __launch_bounds__(kB16Threads, 1)
 
     // ---- phase B
     const uint32_t hb = xs + (uint32_t)warp * a.hb_bytes;
-    uint8_t *hbp = smem + L.x + (size_t)warp * a.hb_bytes;
+    const int nJobs = T > kB16JobTok ? misc[4] : U;
     for (int si = 0; si < myStrips; ++si) {
       const int row0 = (blockIdx.x + si * G) * R, nr = min(R, H - row0);
-      const int J = si * U;
-      for (int u = (warp - J % kB16Warps + kB16Warps) % kB16Warps; u < U && ok; u += kB16Warps) {
-        const uint32_t mask = tokmask[u];
-        const int ntok = __popc(mask);
-        float acc[2][2][4] = {};
+      const int J = si * nJobs;
+      for (int j = (warp - J % kB16Warps + kB16Warps) % kB16Warps; j < nJobs && ok; j += kB16Warps) {
+        int u = j;
+        uint32_t mask;  // the job's tokens
+        if (T > kB16JobTok) {
+          u = jobs[j] & 255;
+          mask = tokmask[u];
+          for (int i = 0; i < (jobs[j] >> 8) * kB16JobTok; ++i) mask &= mask - 1u;
+        } else {
+          mask = tokmask[u];
+        }
+        const int m = min(__popc(mask), kB16JobTok);
+        const int my_t = nth_bit(mask, min(lane, m - 1));  // lane n: token n of the job and its row
+        const int my_row = my_t * kk + slot_j[u * 16 + my_t];
+        int fc = kB16KC, sh = 3;  // inputs whose h fits the warp's buffer; log2(fc / 64)
+        while ((uint32_t)(m * (fc * 2 + 16) * 2) > a.hb_bytes) fc >>= 1, --sh;
         for (int c = 0; c < CB && ok; ++c) {
-          const int o = nA + (J + u) * CB + c, s = o % nst, cc = min(kB16KC, F - c * kB16KC);
-          const uint32_t wa = ring + (uint32_t)s * kB16Stage;
+          const int o = nA + (J + j) * CB + c, cc = min(kB16KC, F - c * kB16KC);
+          const uint32_t wa = ring + (uint32_t)(o & (nst - 1)) * kB16Stage;
           bool landed = false;
-#pragma unroll
-          for (int nb = 0; nb < 2; ++nb) {
-            if (8 * nb >= ntok) break;
-            const int m = min(8, ntok - 8 * nb);  // tokens of this block
-            int fc = kB16KC;                      // inputs whose h fits the warp's buffer
-            while ((uint32_t)(m * (fc * 2 + 16) * 2) > a.hb_bytes) fc >>= 1;
-            for (int k1 = 0; k1 < cc && ok; k1 += fc) {
-              const int kc = min(fc, cc - k1), per = kc / 64;  // 16-byte word pairs of a token per lane
-              const uint32_t hp = (uint32_t)(kc * 2 + 16);     // bytes between tokens
-              const uint32_t lo_off = (uint32_t)m * hp;
-              __syncwarp();
-              for (int i0 = 0; i0 < m * per && ok; i0 += 8) {
-                unsigned long long wv[8][2];
-                uint32_t src[8];  // in pairs of words (at most 256 rows of 2^20)
+          float acc[4][4] = {};
+          for (int k1 = 0; k1 < cc && ok; k1 += fc) {
+            const int kc = min(fc, cc - k1), per = kc / 64;  // 16-byte word pairs of a token per lane
+            const uint32_t hp = (uint32_t)(kc * 2 + 16), lo_off = (uint32_t)m * hp;
+            __syncwarp();
+            for (int n0 = 0; n0 < m && ok; n0 += 8 >> sh) {  // eight loads a lane in flight
+              unsigned long long wv[8][2];
+              uint32_t spins = 0;
+              while (true) {  // all of the words, again until all are this call's
+                bool mine = true;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                  const int n = min((i0 + i) / per, m - 1), p = (i0 + i) % per;
-                  const int t = nth_bit(mask, 8 * nb + n);
-                  src[i] = (uint32_t)(((t * kk + slot_j[u * 16 + t]) * F + c * kB16KC + k1) / 2 + p * 32 + lane);
+                  const int n = n0 + (i >> sh), p = i & ((1 << sh) - 1);
+                  const int row = __shfl_sync(0xffffffffu, my_row, n);
+                  if (n < m && p < per)
+                    ld_relaxed_u64x2(a.hbuf + (size_t)row * F + c * kB16KC + k1 + p * 64 + lane * 2, wv[i][0], wv[i][1]);
                 }
-                uint32_t spins = 0;
-                while (true) {
-                  bool mine = true;
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (i0 + i < m * per) ld_relaxed_u64x2(a.hbuf + 2 * (size_t)src[i], wv[i][0], wv[i][1]);
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (i0 + i < m * per && ((unsigned int)wv[i][0] != epoch || (unsigned int)wv[i][1] != epoch)) mine = false;
-                  if (__all_sync(0xffffffffu, mine)) break;
-                  ++spins;
-                  if (spins > kB16Polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
-                  if (__any_sync(0xffffffffu, spins > kB16Polls || misc[0])) {
-                    ok = false;
-                    break;
-                  }
-                  __nanosleep(64);
+                for (int i = 0; i < 8; ++i)
+                  if (n0 + (i >> sh) < m && (i & ((1 << sh) - 1)) < per &&
+                      ((unsigned int)wv[i][0] != epoch || (unsigned int)wv[i][1] != epoch))
+                    mine = false;
+                if (__all_sync(0xffffffffu, mine)) break;
+                if (++spins > kB16Polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
+                if (__any_sync(0xffffffffu, spins > kB16Polls || misc[0])) {
+                  ok = false;
+                  break;
                 }
-                if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  if (i0 + i >= m * per) break;
-                  const int n = (i0 + i) / per, p = (i0 + i) % per;
-                  const float h0 = __uint_as_float((uint32_t)(wv[i][0] >> 32)), h1 = __uint_as_float((uint32_t)(wv[i][1] >> 32));
-                  const uint32_t hi = cvt_bf16x2(h0, h1);
-                  const uint32_t lo = cvt_bf16x2(h0 - __uint_as_float(hi << 16), h1 - __uint_as_float(hi & 0xFFFF0000u));
-                  const uint32_t at = (uint32_t)n * hp + (uint32_t)(p * 32 + lane) * 4u;
-                  *reinterpret_cast<uint32_t *>(hbp + at) = hi;
-                  *reinterpret_cast<uint32_t *>(hbp + lo_off + at) = lo;
-                }
-              }
-              __syncwarp();
-              if (ok && !landed) {
-                ok = __all_sync(0xffffffffu, wait_full(o));
-                landed = true;
+                __nanosleep(64);
               }
               if (!ok) break;
-              uint32_t ha = hb + (uint32_t)min(g, m - 1) * hp + 32u * t4;
-              int line = (k1 / 64) * R + g;  // 128-byte line of row g; its swizzle is the line's place among eight
-#pragma unroll 4
-              for (int b = 0; b < kc / 64; ++b, line += R, ha += 128) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint32_t wk = wa + (uint32_t)(line * 128 + (((2 * t4 + i) ^ (line & 7)) << 4));
-                  const uint4 w0 = lds_u4(wk), w1 = lds_u4(wk + 1024);
-                  const uint4 vh = lds_u4(ha + 16 * i), vl = lds_u4(ha + lo_off + 16 * i);
-                  const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
-                  mma_bf16_16816(acc[nb][0], f0r, vh.x, vh.y);
-                  mma_bf16_16816(acc[nb][1], f1r, vh.z, vh.w);
-                  mma_bf16_16816(acc[nb][0], f0r, vl.x, vl.y);
-                  mma_bf16_16816(acc[nb][1], f1r, vl.z, vl.w);
+              for (int i = 0; i < 8; ++i) {
+                const int n = n0 + (i >> sh), p = i & ((1 << sh) - 1);
+                if (n < m && p < per) {
+                  const uint32_t at = hb + (uint32_t)n * hp + (uint32_t)(p * 32 + lane) * 4u;
+                  const uint32_t p0 = (uint32_t)(wv[i][0] >> 32), p1 = (uint32_t)(wv[i][1] >> 32);
+                  sts_b32(at, __byte_perm(p0, p1, 0x5410));           // the hi halves
+                  sts_b32(at + lo_off, __byte_perm(p0, p1, 0x7632));  // the lo halves
                 }
               }
             }
-          }
-          __syncwarp();
-          if (ok && lane == 0) mbar_arrive(&empty[s]);
-        }
-        if (!ok) break;
+            __syncwarp();
+            if (ok && !landed) {
+              ok = __all_sync(0xffffffffu, wait_full(o));
+              landed = true;
+            }
+            if (!ok) break;
+            uint32_t ha = hb + (uint32_t)min(g, m - 1) * hp + 32u * t4;
+            int line = (k1 / 64) * R + g;  // 128-byte line of row g; its swizzle is the line's place among eight
+#pragma unroll 2
+            for (int b = 0; b < kc / 64; ++b, line += R, ha += 128) {
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int n = nb * 8 + 2 * t4 + i;
-            if (n < ntok) {
-              const int t = nth_bit(mask, n);
-              float *rb = rowbuf + (t * kk + slot_j[u * 16 + t]) * 16;
-              rb[g] = acc[nb][0][i] + acc[nb][1][i];
-              rb[g + 8] = acc[nb][0][2 + i] + acc[nb][1][2 + i];
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t wk = wa + (uint32_t)(line * 128 + (((2 * t4 + i) ^ (line & 7)) << 4));
+                const uint4 w0 = lds_u4(wk), w1 = lds_u4(wk + 1024);
+                const uint4 vh = lds_u4(ha + 16 * i), vl = lds_u4(ha + lo_off + 16 * i);
+                const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+                mma_bf16_16816(acc[0], f0r, vh.x, vh.y);
+                mma_bf16_16816(acc[1], f1r, vh.z, vh.w);
+                mma_bf16_16816(acc[2], f0r, vl.x, vl.y);
+                mma_bf16_16816(acc[3], f1r, vl.z, vl.w);
+              }
             }
           }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[o & (nst - 1)]);
+          // this chunk's sums, added to those of the earlier inputs
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int n = 2 * t4 + i;
+            const int row = __shfl_sync(0xffffffffu, my_row, n);
+            if (n < m) {
+              float *rb = rowbuf + row * 16 + g;
+              const float s0 = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
+              const float s1 = (acc[0][2 + i] + acc[1][2 + i]) + (acc[2][2 + i] + acc[3][2 + i]);
+              rb[0] = c ? rb[0] + s0 : s0;
+              rb[8] = c ? rb[8] + s1 : s1;
+            }
+          }
+        }
       }
       b16_consumer_sync();  // every expert's rows of this strip are in rowbuf
       if (!misc[0]) {
@@ -598,9 +630,9 @@ static moe_status decode_bf16_launch(DecodeBf16Args &a, cudaStream_t stream) {
   cudaDeviceGetAttribute(&smem_max, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
   const uint32_t cap = (uint32_t)smem_max;
   a.hb_bytes = b16_hb_bytes(a.T);
-  a.nst = kB16MaxStages;
-  while (a.nst > 2 && b16_layout(a.T, a.kk, a.H, a.nst).total > cap) --a.nst;
-  const B16Smem L = b16_layout(a.T, a.kk, a.H, a.nst);
+  a.nst_log2 = 3;
+  while (a.nst_log2 > 1 && b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2).total > cap) --a.nst_log2;
+  const B16Smem L = b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2);
   if (L.total > cap) return MOE_ERR_UNSUPPORTED_SHAPE;
   static std::atomic<int> per_sm[64];  // per device: the shared-memory opt-in and the CTAs per SM it allows
   if (dev < 0 || dev >= 64) {
