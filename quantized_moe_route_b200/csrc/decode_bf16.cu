@@ -28,8 +28,8 @@
 // 128-byte swizzle (piece p of row r at p ^ (r mod 8)) and token rows lie 16
 // bytes (mod 128) apart, so in both the eight lanes of a 16-byte read touch
 // every bank once.  The down projection takes h as a pair of bf16 values (hi +
-// lo, 16 significant bits): the second product is free in a kernel bound by its
-// stream.
+// lo, 16 significant bits) in two token columns of the same instruction, which
+// costs nothing with at most four tokens to a job.
 //
 // The router's logits are computed over the grid (each CTA its experts' rows,
 // K split over the warps, partial sums added in warp order), published as
@@ -72,19 +72,21 @@ struct DecodeBf16Args {
   int nst_log2;                // ring stages
   int R;                       // output channels of a phase B strip (at most 16)
   uint32_t hb_bytes;           // per-warp h buffer
+  int shared_xh;               // the h buffers take x's place after phase A (both do not fit)
 };
 
 struct B16Smem {
-  uint32_t x, rows, tables, total;  // byte offsets; the ring is at 0
+  uint32_t x, h, rows, tables, total;  // byte offsets; the ring is at 0
 };
 __host__ __device__ inline uint32_t b16_hb_bytes(int T) {  // 512 h values (hi and lo) of a token or two, 256 of four
   return T == 1 ? 2080u : 4224u;
 }
-__host__ __device__ inline B16Smem b16_layout(int T, int kk, int H, int nst) {
+__host__ __device__ inline B16Smem b16_layout(int T, int kk, int H, int nst, int shared_xh) {
   B16Smem L;
   L.x = (uint32_t)nst * kB16Stage;
   const uint32_t xb = (uint32_t)T * (uint32_t)(H * 2 + 16), hb = kB16Warps * b16_hb_bytes(T);
-  L.rows = L.x + (xb > hb ? xb : hb);  // x in phase A, the warps' h in phase B
+  L.h = shared_xh ? L.x : L.x + xb;  // x in phase A, the warps' h in phase B
+  L.rows = L.x + (shared_xh ? (xb > hb ? xb : hb) : xb + hb);
   L.tables = L.rows + (uint32_t)(T * kk) * 64u;
   L.total = L.tables + 32 * 4 + 256 * 4 + 256 * 16 + 256 * 4 + 256 * 4 + 256 * 4 + 320 * 2 + 2 * 8 * kB16MaxStages + 64 + 1024 /* alignment of the ring */;
   return L;
@@ -103,18 +105,22 @@ __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
   return __ffs(m) - 1;
 }
 
-// kRows: weight rows of a phase A unit, half gate and half up (8: up to 8
-// tokens; 16: two token columns of 8).  PER: logits per lane in the routing.
+// kRows: weight rows of a phase A unit, half gate and half up.  8 serves up to
+// 4 tokens: the finer units balance the little work there is, and the idle
+// halves of the instruction (rows 8-15, token columns 4-7) take the second
+// half of the unit's inputs, so that one instruction does the work of two.
+// PER: logits per lane in the routing.
 template <int kRows, int PER>
 __global__ void __launch_bounds__(kB16Threads, 1)
     decode_bf16_kernel(DecodeBf16Args a, const __grid_constant__ CUtensorMap gu_map,
                        const __grid_constant__ CUtensorMap dn_map) {
   constexpr int NB = kRows == 16 ? 2 : 1;        // token blocks of 8
+  constexpr bool kJobs = kRows == 16;            // phase B jobs are groups of an expert's tokens
   constexpr int FPU = kRows / 2;                 // features of a unit
   constexpr int KCA = kRows == 16 ? kB16KC : 2 * kB16KC;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const B16Smem L = b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2);
+  uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (keeps the address space known)
+  const B16Smem L = b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2, a.shared_xh);
   float *rowbuf = reinterpret_cast<float *>(smem + L.rows);            // [T kk][16]
   uint32_t *emask = reinterpret_cast<uint32_t *>(smem + L.tables);     // [32] expert presence bits
   uint32_t *tokmask = emask + 32;                                      // [256] tokens of a slot
@@ -178,11 +184,11 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         const uint4 q0 = g < T ? *reinterpret_cast<const uint4 *>(a.x + (size_t)g * H + c) : z;
         const uint4 q1 = g + 8 < T ? *reinterpret_cast<const uint4 *>(a.x + (size_t)(g + 8) * H + c) : z;
         const uint32_t f0[4] = {w0.x, w1.x, w0.y, w1.y}, f1[4] = {w0.z, w1.z, w0.w, w1.w};
-        mma_bf16_16816(d[0], f0, q0.x, q0.y);
-        mma_bf16_16816(d[0], f1, q0.z, q0.w);
+        mma_bf16_pure(d[0], f0, q0.x, q0.y);
+        mma_bf16_pure(d[0], f1, q0.z, q0.w);
         if (NB == 2) {
-          mma_bf16_16816(d[1], f0, q1.x, q1.y);
-          mma_bf16_16816(d[1], f1, q1.z, q1.w);
+          mma_bf16_pure(d[1], f0, q1.x, q1.y);
+          mma_bf16_pure(d[1], f1, q1.z, q1.w);
         }
       }
       float *p = part + warp * 256;
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         }
       }
       int nJobs = U;
-      if (ok && myStrips && T > kB16JobTok) {
+      if (ok && myStrips && kJobs) {
         for (uint32_t i = 0; !misc[3] && ok; ++i) {
           if (i > kB16Polls) fail(DEVERR_DECODE_H_WAIT);
           ok = !misc[0];
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
       for (int si = 0; si < myStrips && ok; ++si) {
         const int row0 = (blockIdx.x + si * G) * R;
         for (int j = 0; j < nJobs && ok; ++j) {
-          const int e = slot_expert[T > kB16JobTok ? jobs[j] & 255 : j];
+          const int e = slot_expert[kJobs ? jobs[j] & 255 : j];
           for (int c = 0; c < CB && (ok = arm((uint32_t)R * (kB16KC * 2))); ++c) {
             const int s = (ord - 1) & (nst - 1);
             tma_load_4d_hint(smem + (size_t)s * kB16Stage, &dn_map, 0, row0, c * (kB16KC / 64), e, &full[s], pol);
@@ -382,7 +388,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
       }
     }
     b16_consumer_sync();
-    if (T > kB16JobTok && warp == kB16Warps - 1) {  // the jobs of phase B; eight slots a lane
+    if (kJobs && warp == kB16Warps - 1) {  // the jobs of phase B; eight slots a lane
       int n = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) n += (__popc(tokmask[8 * lane + i]) + kB16JobTok - 1) / kB16JobTok;
@@ -398,17 +404,18 @@ __global__ void __launch_bounds__(kB16Threads, 1)
     }
     bool ok = true;
     // ---- phase A
-    const uint32_t ring = smem_u32(smem), xs = smem_u32(smem + L.x);
+    const uint8_t *xs = smem + L.x;
+    auto ld16 = [](const uint8_t *p) { return *reinterpret_cast<const uint4 *>(p); };
     // this lane's pieces 2 t and 2 t + 1 of row g (or g + 8) of a swizzled 8-row group
     const uint32_t wo[2] = {(uint32_t)(g * 128 + (((2 * t4) ^ g) << 4)), (uint32_t)(g * 128 + (((2 * t4 + 1) ^ g) << 4))};
     for (int q = warp; q < myUnits && ok; q += kB16Warps) {
       const int unit = blockIdx.x + q * G, slot = unit / UA, f0 = (unit - slot * UA) * FPU;
       const uint32_t mask = tokmask[slot];
       const int ntok = __popc(mask);
-      uint32_t xa[NB];
+      const uint8_t *xa[NB];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
-        const int n = nb * 8 + g;
+        const int n = kRows == 16 ? nb * 8 + g : (g & 3);
         xa[nb] = xs + (uint32_t)nth_bit(mask, n < ntok ? n : 0) * xpitch + 32u * t4;
       }
       const bool two = NB == 2 && ntok > 8;
@@ -419,22 +426,40 @@ __global__ void __launch_bounds__(kB16Threads, 1)
           ok = false;
           break;
         }
-        uint32_t wa = ring + (uint32_t)s * kB16Stage;
+        const uint8_t *wa = smem + (uint32_t)s * kB16Stage;
         const int nch = min(KCA, H - c * KCA) / 64;
         uint32_t xo = (uint32_t)(c * KCA * 2);
+        if (kRows == 16) {
 #pragma unroll 4
-        for (int b = 0; b < nch; ++b, wa += kRows * 128, xo += 128) {
+          for (int b = 0; b < nch; ++b, wa += 2048, xo += 128) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 w0 = lds_u4(wa + wo[i]);
-            const uint4 w1 = kRows == 16 ? lds_u4(wa + 1024 + wo[i]) : make_uint4(0, 0, 0, 0);
-            const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+            for (int i = 0; i < 2; ++i) {
+              const uint4 w0 = ld16(wa + wo[i]), w1 = ld16(wa + 1024 + wo[i]);
+              const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              if (nb == 1 && !two) continue;
-              const uint4 v = lds_u4(xa[nb] + xo + 16 * i);
-              mma_bf16_16816(acc[nb][2 * i], f0r, v.x, v.y);
-              mma_bf16_16816(acc[nb][2 * i + 1], f1r, v.z, v.w);
+              for (int nb = 0; nb < NB; ++nb) {
+                if (nb == 1 && !two) continue;
+                const uint4 v = ld16(xa[nb] + xo + 16 * i);
+                mma_bf16_pure(acc[nb][2 * i], f0r, v.x, v.y);
+                mma_bf16_pure(acc[nb][2 * i + 1], f1r, v.z, v.w);
+              }
+            }
+          }
+        } else {
+          // rows 0-7 with tokens 0-3: columns b; rows 8-15 (the same weight rows)
+          // with tokens in 4-7: columns b + half.  An odd last column meets
+          // zeros (out of range, filled by the copy), with any x that exists.
+          const int half = (nch + 1) / 2;
+#pragma unroll 4
+          for (int b = 0; b < half; ++b, wa += 1024, xo += 128) {
+            const uint8_t *xv = xa[0] + xo + (g >= 4 && b + half < nch ? half * 128 : 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 w0 = ld16(wa + wo[i]), w1 = ld16(wa + half * 1024 + wo[i]);
+              const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+              const uint4 v = ld16(xv + 16 * i);
+              mma_bf16_pure(acc[0][2 * i], f0r, v.x, v.y);
+              mma_bf16_pure(acc[0][2 * i + 1], f1r, v.z, v.w);
             }
           }
         }
@@ -447,7 +472,9 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = (acc[nb][0][i] + acc[nb][1][i]) + (acc[nb][2][i] + acc[nb][3][i]);
-        if (kRows == 8) {  // rows 0-3 gate, 4-7 up: the partner is 16 lanes up
+        if (kRows == 8) {  // the halves' sums; rows 0-3 gate, 4-7 up: the partner is 16 lanes up
+          v[0] += __shfl_down_sync(0xffffffffu, v[2], 2);
+          v[1] += __shfl_down_sync(0xffffffffu, v[3], 2);
           v[2] = __shfl_down_sync(0xffffffffu, v[0], 16);
           v[3] = __shfl_down_sync(0xffffffffu, v[1], 16);
         }
@@ -465,18 +492,18 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         }
       }
     }
-    b16_consumer_sync();  // x is consumed: its space holds the warps' h now
+    if (a.shared_xh || kJobs) b16_consumer_sync();  // x is consumed and the jobs are listed
 
     // ---- phase B
-    const uint32_t hb = xs + (uint32_t)warp * a.hb_bytes;
-    const int nJobs = T > kB16JobTok ? misc[4] : U;
+    uint8_t *hbp = smem + L.h + (uint32_t)warp * a.hb_bytes;
+    const int nJobs = kJobs ? misc[4] : U;
     for (int si = 0; si < myStrips; ++si) {
       const int row0 = (blockIdx.x + si * G) * R, nr = min(R, H - row0);
       const int J = si * nJobs;
-      for (int j = (warp - J % kB16Warps + kB16Warps) % kB16Warps; j < nJobs && ok; j += kB16Warps) {
+      for (int j = (2 * kB16Warps - 1 - warp - J % kB16Warps) % kB16Warps; j < nJobs && ok; j += kB16Warps) {
         int u = j;
         uint32_t mask;  // the job's tokens
-        if (T > kB16JobTok) {
+        if (kJobs) {
           u = jobs[j] & 255;
           mask = tokmask[u];
           for (int i = 0; i < (jobs[j] >> 8) * kB16JobTok; ++i) mask &= mask - 1u;
@@ -490,7 +517,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         while ((uint32_t)(m * (fc * 2 + 16) * 2) > a.hb_bytes) fc >>= 1, --sh;
         for (int c = 0; c < CB && ok; ++c) {
           const int o = nA + (J + j) * CB + c, cc = min(kB16KC, F - c * kB16KC);
-          const uint32_t wa = ring + (uint32_t)(o & (nst - 1)) * kB16Stage;
+          const uint8_t *wa = smem + (uint32_t)(o & (nst - 1)) * kB16Stage;
           bool landed = false;
           float acc[4][4] = {};
           for (int k1 = 0; k1 < cc && ok; k1 += fc) {
@@ -500,6 +527,15 @@ __global__ void __launch_bounds__(kB16Threads, 1)
             for (int n0 = 0; n0 < m && ok; n0 += 8 >> sh) {  // eight loads a lane in flight
               unsigned long long wv[8][2];
               uint32_t spins = 0;
+              // warps that are early (no barrier before phase B) poll one row of
+              // words while h is far off: all of them would crowd the stream
+              while (!a.shared_xh) {
+                const int row = __shfl_sync(0xffffffffu, my_row, n0);
+                ld_relaxed_u64x2(a.hbuf + (size_t)row * F + c * kB16KC + k1 + lane * 2, wv[0][0], wv[0][1]);
+                if (__all_sync(0xffffffffu, (unsigned int)wv[0][0] == epoch && (unsigned int)wv[0][1] == epoch)) break;
+                if (++spins > kB16Polls || __any_sync(0xffffffffu, misc[0])) break;  // (the loop below ends the wait)
+                __nanosleep(100);
+              }
               while (true) {  // all of the words, again until all are this call's
                 bool mine = true;
 #pragma unroll
@@ -527,10 +563,10 @@ __global__ void __launch_bounds__(kB16Threads, 1)
               for (int i = 0; i < 8; ++i) {
                 const int n = n0 + (i >> sh), p = i & ((1 << sh) - 1);
                 if (n < m && p < per) {
-                  const uint32_t at = hb + (uint32_t)n * hp + (uint32_t)(p * 32 + lane) * 4u;
+                  uint8_t *at = hbp + (uint32_t)n * hp + (uint32_t)(p * 32 + lane) * 4u;
                   const uint32_t p0 = (uint32_t)(wv[i][0] >> 32), p1 = (uint32_t)(wv[i][1] >> 32);
-                  sts_b32(at, __byte_perm(p0, p1, 0x5410));           // the hi halves
-                  sts_b32(at + lo_off, __byte_perm(p0, p1, 0x7632));  // the lo halves
+                  *reinterpret_cast<uint32_t *>(at) = __byte_perm(p0, p1, 0x5410);           // the hi halves
+                  *reinterpret_cast<uint32_t *>(at + lo_off) = __byte_perm(p0, p1, 0x7632);  // the lo halves
                 }
               }
             }
@@ -540,37 +576,39 @@ __global__ void __launch_bounds__(kB16Threads, 1)
               landed = true;
             }
             if (!ok) break;
-            uint32_t ha = hb + (uint32_t)min(g, m - 1) * hp + 32u * t4;
+            // token columns 0-3 take hi, 4-7 lo of the job's tokens
+            const uint8_t *ha = hbp + (uint32_t)min(g & 3, m - 1) * hp + (g >= 4 ? lo_off : 0u) + 32u * t4;
             int line = (k1 / 64) * R + g;  // 128-byte line of row g; its swizzle is the line's place among eight
-#pragma unroll 2
+#pragma unroll 4
             for (int b = 0; b < kc / 64; ++b, line += R, ha += 128) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const uint32_t wk = wa + (uint32_t)(line * 128 + (((2 * t4 + i) ^ (line & 7)) << 4));
-                const uint4 w0 = lds_u4(wk), w1 = lds_u4(wk + 1024);
-                const uint4 vh = lds_u4(ha + 16 * i), vl = lds_u4(ha + lo_off + 16 * i);
+                const uint8_t *wk = wa + (line * 128 + (((2 * t4 + i) ^ (line & 7)) << 4));
+                const uint4 w0 = ld16(wk), w1 = ld16(wk + 1024);
+                const uint4 v = ld16(ha + 16 * i);
                 const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
-                mma_bf16_16816(acc[0], f0r, vh.x, vh.y);
-                mma_bf16_16816(acc[1], f1r, vh.z, vh.w);
-                mma_bf16_16816(acc[2], f0r, vl.x, vl.y);
-                mma_bf16_16816(acc[3], f1r, vl.z, vl.w);
+                mma_bf16_pure(acc[2 * i], f0r, v.x, v.y);
+                mma_bf16_pure(acc[2 * i + 1], f1r, v.z, v.w);
               }
             }
           }
           if (!ok) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[o & (nst - 1)]);
-          // this chunk's sums, added to those of the earlier inputs
+          // this chunk's sums (hi + lo), added to those of the earlier inputs
+          float v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
+            v[i] += __shfl_down_sync(0xffffffffu, v[i], 2);
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int n = 2 * t4 + i;
-            const int row = __shfl_sync(0xffffffffu, my_row, n);
+            const int n = 2 * t4 + i, row = __shfl_sync(0xffffffffu, my_row, n);
             if (n < m) {
               float *rb = rowbuf + row * 16 + g;
-              const float s0 = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
-              const float s1 = (acc[0][2 + i] + acc[1][2 + i]) + (acc[2][2 + i] + acc[3][2 + i]);
-              rb[0] = c ? rb[0] + s0 : s0;
-              rb[8] = c ? rb[8] + s1 : s1;
+              rb[0] = c ? rb[0] + v[i] : v[i];
+              rb[8] = c ? rb[8] + v[2 + i] : v[2 + i];
             }
           }
         }
@@ -631,8 +669,10 @@ static moe_status decode_bf16_launch(DecodeBf16Args &a, cudaStream_t stream) {
   const uint32_t cap = (uint32_t)smem_max;
   a.hb_bytes = b16_hb_bytes(a.T);
   a.nst_log2 = 3;
-  while (a.nst_log2 > 1 && b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2).total > cap) --a.nst_log2;
-  const B16Smem L = b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2);
+  a.shared_xh = 0;
+  if (b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2, a.shared_xh).total > cap) a.shared_xh = 1;
+  while (a.nst_log2 > 1 && b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2, a.shared_xh).total > cap) --a.nst_log2;
+  const B16Smem L = b16_layout(a.T, a.kk, a.H, 1 << a.nst_log2, a.shared_xh);
   if (L.total > cap) return MOE_ERR_UNSUPPORTED_SHAPE;
   static std::atomic<int> per_sm[64];  // per device: the shared-memory opt-in and the CTAs per SM it allows
   if (dev < 0 || dev >= 64) {
@@ -731,6 +771,6 @@ extern "C" MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer,
   a.H = H;
   a.F = F;
   cudaStream_t s = as_stream(stream);
-  if (T <= 8) return Er <= 256 ? decode_bf16_launch<8, 8>(a, s) : decode_bf16_launch<8, 32>(a, s);
+  if (T <= kB16JobTok) return Er <= 256 ? decode_bf16_launch<8, 8>(a, s) : decode_bf16_launch<8, 32>(a, s);
   return Er <= 256 ? decode_bf16_launch<16, 8>(a, s) : decode_bf16_launch<16, 32>(a, s);
 }

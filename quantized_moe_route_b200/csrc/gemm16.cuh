@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
   static_assert(!kGated || kMats == 2, "gate and up");
   constexpr int kOut = kGated ? 128 : 128 * kMats;  // outputs per tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (keeps the address space known)
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kTailOff);
   uint64_t *empty = full + kG16Stages;
   uint64_t *acc_full = empty + kG16Stages;  // [2]
