@@ -13,10 +13,10 @@
 //
 // Warp 0 loads 64-channel stages by TMA (128-byte swizzle; out-of-range rows
 // and channels arrive as zeros), warp 1 issues tcgen05.mma into one of two
-// accumulator sets in tensor memory, warps 2-9 run the epilogue of the other
+// accumulator sets in tensor memory, warps 2-13 run the epilogue of the other
 // set.  Products with too few tiles for the GPU split K over a cluster of
 // CTAs instead of looping over tiles: each leaves its fp32 partial in shared
-// memory, and CTA r adds up the rows r, r + S, ... in rank order through
+// memory, and every CTA adds up its share of the rows in rank order through
 // distributed shared memory (a fixed order: the same bits every call).
 #pragma once
 #include "tcgen05.cuh"
@@ -26,7 +26,7 @@ namespace moe {
 
 constexpr int kG16BK = 64;
 constexpr int kG16Stages = 4;
-constexpr int kG16EpiWarps = 8;
+constexpr int kG16EpiWarps = 12;  // three to a lane quarter of tensor memory
 constexpr int kG16Threads = (2 + kG16EpiWarps) * 32;
 constexpr uint32_t kG16WaitPolls = 1u << 18;  // sleeping polls of up to 10 us: a bound of seconds
 
@@ -127,44 +127,95 @@ __device__ __forceinline__ void activate_all(float (&v)[kN], int act) {
   }
 }
 
-// kN rows (row0 + i * step, the first nv of them valid) of output n from
-// their products p0 (and, gated, p1): bias, activation, gate, residual, store.
-template <bool kGated, bool kF16, int kN>
-__device__ __forceinline__ void gemm16_emit(const Gemm16Args &a, int n, int64_t row0, int step, int nv, float (&p0)[kN],
-                                            float (&p1)[kN]) {
-  if (n >= a.N) return;
-  float r[kN];
+// The residual of output n in kN rows from row0 on (the first nv of them exist),
+// as stored.  Issued a batch ahead of its use: its latency is the epilogue's.
+template <int kN>
+__device__ __forceinline__ void gemm16_residual(const Gemm16Args &a, int n, int64_t row0, int nv, uint16_t (&r)[kN]) {
   const uint16_t *rp = a.residual + row0 * a.ldr + n;
-  if (a.residual) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) r[i] = i < nv ? w16_to_f32<kF16>(rp[i * step * a.ldr]) : 0.f;
-  }
-  if (a.bias) {
-    const float b0 = w16_to_f32<kF16>(a.bias[n]);
+  for (int i = 0; i < kN; ++i) r[i] = i < nv && n < a.N ? rp[i * a.ldr] : (uint16_t)0;
+}
+
+// kN rows of output n from their products p0 (and, gated, p1) and residual r:
+// bias (b0, b1), activation, gate, residual, store.
+template <bool kGated, bool kF16, int kN>
+__device__ __forceinline__ void gemm16_emit(const Gemm16Args &a, int n, int64_t row0, int nv, float b0, float b1,
+                                            const uint16_t (&r)[kN], float (&p0)[kN], float (&p1)[kN]) {
+  if (n >= a.N) return;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) p0[i] += b0;
-  }
+  for (int i = 0; i < kN; ++i) p0[i] += b0;
   activate_all(p0, a.act);
   if (kGated) {
-    const float b1 = a.bias ? w16_to_f32<kF16>(a.bias[a.N + n]) : 0.f;
 #pragma unroll
     for (int i = 0; i < kN; ++i) p0[i] *= p1[i] + b1;
   }
   if (a.residual) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) p0[i] += r[i];
+    for (int i = 0; i < kN; ++i) p0[i] += w16_to_f32<kF16>(r[i]);
   }
-  const int64_t o = row0 * a.ldy + n, dy = step * a.ldy;
+  const int64_t o = row0 * a.ldy + n;
   if (a.y_f32) {
     float *y = static_cast<float *>(a.y) + o;
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      if (i < nv) y[i * dy] = p0[i];
+      if (i < nv) y[i * a.ldy] = p0[i];
   } else {
     uint16_t *y = static_cast<uint16_t *>(a.y) + o;
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      if (i < nv) y[i * dy] = f32_to_w16<kF16>(p0[i]);
+      if (i < nv) y[i * a.ldy] = f32_to_w16<kF16>(p0[i]);
+  }
+}
+
+// The biases of output n (gated: of its gate and up rows).
+template <bool kGated, bool kF16>
+__device__ __forceinline__ void gemm16_bias(const Gemm16Args &a, int n, float &b0, float &b1) {
+  b0 = a.bias && n < a.N ? w16_to_f32<kF16>(a.bias[n]) : 0.f;
+  b1 = kGated && a.bias && n < a.N ? w16_to_f32<kF16>(a.bias[a.N + n]) : 0.f;
+}
+
+// A cluster's epilogue: CTA `rank` of kS adds up its share of the tile's rows
+// over the partials of all kS CTAs, in rank order, with the loads of a batch of
+// rows in flight together (a distributed shared-memory load takes about half a
+// microsecond).
+template <int kS, bool kGated, int kMats, int kNT, bool kF16>
+__device__ __forceinline__ void gemm16_join(const Gemm16Args &a, const Gemm16Tile &ti, uint32_t part, int rank) {
+  constexpr int kR = 32 / (kS * kMats);  // rows of a batch
+  constexpr int kSides = kMats == 2 && !kGated ? 2 : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, sub = (warp - 2) >> 2;
+  const int n = ti.n0 + q * 32 + lane;
+  const int per = (ti.nvalid + kS - 1) / kS, c1 = min(ti.nvalid, (rank + 1) * per);
+  part += (uint32_t)(q * 32 + lane) * 4u;
+  float b0[kSides], b1[kSides];
+#pragma unroll
+  for (int m = 0; m < kSides; ++m) gemm16_bias<kGated, kF16>(a, n + 128 * m, b0[m], b1[m]);
+  for (int c = rank * per + sub * kR; c < c1; c += kR * (kG16EpiWarps / 4)) {
+    const int nv = min(kR, c1 - c);
+    uint16_t r[kSides][kR] = {};
+    if (a.residual) {
+#pragma unroll
+      for (int m = 0; m < kSides; ++m) gemm16_residual(a, n + 128 * m, ti.row0 + c, nv, r[m]);
+    }
+    float v[kS][kMats][kR];
+#pragma unroll
+    for (int k = 0; k < kS; ++k)
+#pragma unroll
+      for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int i = 0; i < kR; ++i)
+          v[k][m][i] = i < nv ? ld_dsmem_f32(part + (uint32_t)(m * kNT + c + i) * 512u, k) : 0.f;
+    float p[2][kR];
+#pragma unroll
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        p[m][i] = v[0][m][i];
+#pragma unroll
+        for (int k = 1; k < kS; ++k) p[m][i] += v[k][m][i];
+      }
+    gemm16_emit<kGated, kF16>(a, n, ti.row0 + c, nv, b0[0], b1[0], r[0], p[0], p[kMats - 1]);
+    if (kSides == 2)
+      gemm16_emit<false, kF16>(a, n + 128, ti.row0 + c, nv, b0[kSides - 1], 0.f, r[kSides - 1], p[1], p[1]);
   }
 }
 
@@ -297,22 +348,39 @@ __global__ void __launch_bounds__(kG16Threads, 1)
     }
   } else {
     // epilogue warps: lane quarter q holds outputs 32 q + lane of each block;
-    // the quarter's two warps take alternate groups of 16 rows
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    // the quarter's warps take groups of 16 rows in turn
+    const int q = warp & 3, sub = (warp - 2) >> 2;
+    constexpr int kStep = 16 * (kG16EpiWarps / 4);
     uint32_t tc = 0;
     for (int t = t0; t < ntiles && !*abort_s; t += G, ++tc) {
       const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
+      const int n = ti.n0 + q * 32 + lane;
+      constexpr int kSides = kMats == 2 && !kGated ? 2 : 1;  // outputs n and n + 128
+      float b0[kSides], b1[kSides];
+      uint16_t r[kSides][16] = {};
+      if (S == 1) {  // what does not depend on the products, before waiting for them
+#pragma unroll
+        for (int m = 0; m < kSides; ++m) {
+          gemm16_bias<kGated, kF16>(a, n + 128 * m, b0[m], b1[m]);
+          if (a.residual) gemm16_residual(a, n + 128 * m, ti.row0 + sub * 16, ti.nvalid - sub * 16, r[m]);
+        }
+      }
       if (!mbar_wait_sleep(&acc_full[tc & 1u], (tc >> 1) & 1u, kG16WaitPolls)) {
         fail();
         break;
       }
       tc_fence_after();
       const uint32_t acc = tmem + (tc & 1u) * C::kAccCols + ((uint32_t)(q * 32) << 16);
-      const int n = ti.n0 + q * 32 + lane;
-      for (int c0 = half * 16; c0 < ti.nvalid; c0 += 32) {
+      for (int c0 = sub * 16; c0 < ti.nvalid; c0 += kStep) {
         uint32_t v[kMats][16];
 #pragma unroll
         for (int m = 0; m < kMats; ++m) tmem_ld16_async(acc + m * kNT + c0, v[m]);
+        uint16_t rn[kSides][16];
+        if (a.residual && S == 1) {  // the next batch's
+#pragma unroll
+          for (int m = 0; m < kSides; ++m)
+            gemm16_residual(a, n + 128 * m, ti.row0 + c0 + kStep, ti.nvalid - c0 - kStep, rn[m]);
+        }
         tmem_ld_wait();
         float p[2][16];
 #pragma unroll
@@ -328,9 +396,14 @@ __global__ void __launch_bounds__(kG16Threads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) part[(m * kNT + c0 + i) * 128 + q * 32 + lane] = p[m][i];
         } else {
-          gemm16_emit<kGated, kF16>(a, n, ti.row0 + c0, 1, ti.nvalid - c0, p[0], p[kMats - 1]);
-          if (kMats == 2 && !kGated)
-            gemm16_emit<false, kF16>(a, n + 128, ti.row0 + c0, 1, ti.nvalid - c0, p[1], p[1]);
+          gemm16_emit<kGated, kF16>(a, n, ti.row0 + c0, ti.nvalid - c0, b0[0], b1[0], r[0], p[0], p[kMats - 1]);
+          if (kSides == 2)
+            gemm16_emit<false, kF16>(a, n + 128, ti.row0 + c0, ti.nvalid - c0, b0[kSides - 1], 0.f, r[kSides - 1], p[1],
+                                     p[1]);
+#pragma unroll
+          for (int m = 0; m < kSides; ++m)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[m][i] = rn[m][i];
         }
       }
       tc_fence_before();
@@ -342,17 +415,10 @@ __global__ void __launch_bounds__(kG16Threads, 1)
     cluster_sync_all();
     if (warp >= 2 && t0 < ntiles) {
       const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t0);
-      const int q = warp & 3, half = (warp - 2) >> 2;
-      const int n = ti.n0 + q * 32 + lane;
-      const uint32_t part = smem_u32(smem) + (uint32_t)(q * 32 + lane) * 4u;
-      for (int c = rank + half * S; c < ti.nvalid; c += 2 * S) {
-        float p[2][1] = {};
-#pragma unroll
-        for (int m = 0; m < kMats; ++m)
-          for (int r = 0; r < S; ++r) p[m][0] += ld_dsmem_f32(part + (uint32_t)(m * kNT + c) * 512u, r);
-        gemm16_emit<kGated, kF16>(a, n, ti.row0 + c, 1, 1, p[0], p[kMats - 1]);
-        if (kMats == 2 && !kGated) gemm16_emit<false, kF16>(a, n + 128, ti.row0 + c, 1, 1, p[1], p[1]);
-      }
+      const uint32_t part = smem_u32(smem);
+      if (S == 8) gemm16_join<8, kGated, kMats, kNT, kF16>(a, ti, part, rank);
+      else if (S == 4) gemm16_join<4, kGated, kMats, kNT, kF16>(a, ti, part, rank);
+      else gemm16_join<2, kGated, kMats, kNT, kF16>(a, ti, part, rank);
     }
     cluster_sync_all();  // no CTA leaves while another may read its partials
   }
