@@ -1,7 +1,35 @@
-// linear.cu -- y = act(x w^T + bias) + residual on 16-bit weights.
+// linear.cu -- y = act(x w^T + bias) + residual on 16-bit weights: up to 16
+// rows of x as a weight stream, more on the 5th-generation tensor cores.
 #include "gemm16.cuh"
+#include "linear_stream.cuh"
 
 namespace moe {
+
+constexpr int kLinearStreamRows = 16;
+
+template <bool kGated, bool kF16>
+static moe_status linear_stream(const Gemm16Args &g, const void *x, int64_t ldx, const void *w, int64_t ldw, cudaStream_t s) {
+  DeviceInfo d;
+  if (!device_info(&d)) return MOE_ERR_CUDA;
+  // equal strips: as few to an SM as 16 rows each allow, of as few rows as that takes
+  const int most = kGated ? 8 : 16;
+  const int per_sm = (g.N + most * d.sms - 1) / (most * d.sms), per = (g.N + per_sm * d.sms - 1) / (per_sm * d.sms);
+  LinearStreamArgs a;
+  a.g = g;
+  a.R = kGated ? 2 * per : per;
+  a.strips = (g.N + per - 1) / per;
+  a.group_log2 = g.K > 512 ? 4 : g.K > 256 ? 3 : 2;  // 64 inputs a warp at least
+  CUtensorMap wm, xm;
+  const bool two = g.rows > 8;
+  if (!gemm16_map(&wm, w, (int64_t)g.N * (kGated ? 2 : 1), g.K, ldw, per, kF16) ||
+      !gemm16_map(&xm, x, g.rows, g.K, ldx, two ? 16 : 8, kF16)) {
+    set_cuda_error(cudaErrorInvalidValue);
+    return MOE_ERR_CUDA;
+  }
+  const int grid = a.strips < d.sms ? a.strips : d.sms;
+  return two ? linear_stream_launch<kGated, kF16, 2>(a, grid, wm, xm, d.dev, s)
+             : linear_stream_launch<kGated, kF16, 1>(a, grid, wm, xm, d.dev, s);
+}
 
 template <bool kGated, bool kF16>
 static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const void *w, int64_t ldw, cudaStream_t s) {
@@ -65,6 +93,11 @@ extern "C" MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void 
   a.err = device_error_word();
   if (!a.err) return MOE_ERR_CUDA;
   cudaStream_t s = as_stream(stream);
-  if (dtype == MOE_F16) return gated ? linear_gemm<true, true>(a, x, ldx, w, ldw, s) : linear_gemm<false, true>(a, x, ldx, w, ldw, s);
+  const bool f16 = dtype == MOE_F16;
+  if (T <= kLinearStreamRows) {
+    if (f16) return gated ? linear_stream<true, true>(a, x, ldx, w, ldw, s) : linear_stream<false, true>(a, x, ldx, w, ldw, s);
+    return gated ? linear_stream<true, false>(a, x, ldx, w, ldw, s) : linear_stream<false, false>(a, x, ldx, w, ldw, s);
+  }
+  if (f16) return gated ? linear_gemm<true, true>(a, x, ldx, w, ldw, s) : linear_gemm<false, true>(a, x, ldx, w, ldw, s);
   return gated ? linear_gemm<true, false>(a, x, ldx, w, ldw, s) : linear_gemm<false, false>(a, x, ldx, w, ldw, s);
 }
