@@ -146,6 +146,8 @@ __global__ void __launch_bounds__(kB16Threads, 1)
     misc[2] = 0;
     misc[3] = 0;
     fence_mbar_init();
+    tma_prefetch_map(&gu_map);
+    tma_prefetch_map(&dn_map);
   }
   if (tid < 32) emask[tid] = 0u;
   if (tid < 256) tokmask[tid] = 0u;
@@ -154,11 +156,6 @@ __global__ void __launch_bounds__(kB16Threads, 1)
     const unsigned int ep = a.ctrl[0] + 1u;  // this call's epoch; never 0 (zeroed words never match)
     misc[1] = (int)(ep == 0u ? 1u : ep);
   }
-  for (int v = tid; v < T * (H / 8); v += kB16Threads) {
-    const int t = v / (H / 8), c = v - t * (H / 8);
-    cp_async_16(smem + L.x + (size_t)t * xpitch + 16 * c, a.x + (size_t)t * H + 8 * c);
-  }
-  cp_async_commit();
   auto fail = [&](int code) {
     atomicExch(a.err, code);
     misc[0] = 1;
@@ -216,6 +213,11 @@ __global__ void __launch_bounds__(kB16Threads, 1)
       __syncthreads();
     }
     fence_proxy_async_smem();  // the ring's next writers are the weight copies
+  }
+  if (warp < T) {  // token `warp` of x; awaited after the routing
+    const uint16_t *src = a.x + (size_t)warp * H;
+    for (int c = lane; c < H / 8; c += 32) cp_async_16(smem + L.x + (size_t)warp * xpitch + 16 * c, src + 8 * c);
+    cp_async_commit();
   }
   __syncthreads();  // barrier initialisation, table clears, the epoch
   const unsigned int epoch = (unsigned int)misc[1];

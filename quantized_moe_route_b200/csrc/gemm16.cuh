@@ -68,11 +68,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ float4 ld_dsmem_f32x4(uint32_t addr, uint32_t rank) {
   uint32_t a;
-  float v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
   return v;
 }
 
@@ -174,48 +177,85 @@ __device__ __forceinline__ void gemm16_bias(const Gemm16Args &a, int n, float &b
   b1 = kGated && a.bias && n < a.N ? w16_to_f32<kF16>(a.bias[a.N + n]) : 0.f;
 }
 
+// Four consecutive outputs n .. n + 3 of row `row` (those below a.N), from their
+// products: as gemm16_emit, with the row's outputs in one vector where they
+// lie on its boundary.
+template <bool kGated, bool kF16>
+__device__ __forceinline__ void gemm16_emit4(const Gemm16Args &a, int n, int64_t row, float (&p0)[4], float (&p1)[4]) {
+  if (n >= a.N) return;
+  const int nv = min(4, a.N - n);
+  float b[2][4] = {};
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < nv) b[0][i] = w16_to_f32<kF16>(a.bias[n + i]);
+      if (kGated && i < nv) b[1][i] = w16_to_f32<kF16>(a.bias[a.N + n + i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p0[i] += b[0][i];
+  activate_all(p0, a.act);
+  if (kGated) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p0[i] *= p1[i] + b[1][i];
+  }
+  if (a.residual) {
+    const uint16_t *r = a.residual + row * a.ldr + n;
+    if (nv == 4 && reinterpret_cast<uintptr_t>(r) % 8 == 0) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(r);
+      const uint32_t u[2] = {v.x, v.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p0[i] += w16_to_f32<kF16>((uint16_t)(u[i >> 1] >> (16 * (i & 1))));
+    } else {
+      for (int i = 0; i < nv; ++i) p0[i] += w16_to_f32<kF16>(r[i]);
+    }
+  }
+  if (a.y_f32) {
+    float *y = static_cast<float *>(a.y) + row * a.ldy + n;
+    if (nv == 4 && reinterpret_cast<uintptr_t>(y) % 16 == 0)
+      *reinterpret_cast<float4 *>(y) = make_float4(p0[0], p0[1], p0[2], p0[3]);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < nv) y[i] = p0[i];
+  } else {
+    uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.ldy + n;
+    uint16_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f32_to_w16<kF16>(p0[i]);
+    if (nv == 4 && reinterpret_cast<uintptr_t>(y) % 8 == 0)
+      *reinterpret_cast<uint2 *>(y) = make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < nv) y[i] = o[i];
+  }
+}
+
 // A cluster's epilogue: CTA `rank` of kS adds up its share of the tile's rows
-// over the partials of all kS CTAs, in rank order, with the loads of a batch of
-// rows in flight together (a distributed shared-memory load takes about half a
-// microsecond).
+// over the partials of all kS CTAs, in rank order: a warp takes a row, a lane
+// four of its 128 outputs, with the loads from all CTAs in flight together.
 template <int kS, bool kGated, int kMats, int kNT, bool kF16>
 __device__ __forceinline__ void gemm16_join(const Gemm16Args &a, const Gemm16Tile &ti, uint32_t part, int rank) {
-  constexpr int kR = 32 / (kS * kMats);  // rows of a batch
-  constexpr int kSides = kMats == 2 && !kGated ? 2 : 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, sub = (warp - 2) >> 2;
-  const int n = ti.n0 + q * 32 + lane;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (ti.nvalid + kS - 1) / kS, c1 = min(ti.nvalid, (rank + 1) * per);
-  part += (uint32_t)(q * 32 + lane) * 4u;
-  float b0[kSides], b1[kSides];
-#pragma unroll
-  for (int m = 0; m < kSides; ++m) gemm16_bias<kGated, kF16>(a, n + 128 * m, b0[m], b1[m]);
-  for (int c = rank * per + sub * kR; c < c1; c += kR * (kG16EpiWarps / 4)) {
-    const int nv = min(kR, c1 - c);
-    uint16_t r[kSides][kR] = {};
-    if (a.residual) {
-#pragma unroll
-      for (int m = 0; m < kSides; ++m) gemm16_residual(a, n + 128 * m, ti.row0 + c, nv, r[m]);
-    }
-    float v[kS][kMats][kR];
+  part += (uint32_t)lane * 16u;
+  for (int c = rank * per + warp - 2; c < c1; c += kG16EpiWarps) {
+    float4 v[kS][kMats];
 #pragma unroll
     for (int k = 0; k < kS; ++k)
 #pragma unroll
-      for (int m = 0; m < kMats; ++m)
+      for (int m = 0; m < kMats; ++m) v[k][m] = ld_dsmem_f32x4(part + (uint32_t)(m * kNT + c) * 512u, k);
+    float p[kMats][4];
 #pragma unroll
-        for (int i = 0; i < kR; ++i)
-          v[k][m][i] = i < nv ? ld_dsmem_f32(part + (uint32_t)(m * kNT + c + i) * 512u, k) : 0.f;
-    float p[2][kR];
+    for (int m = 0; m < kMats; ++m) {
+      float4 t = v[0][m];
 #pragma unroll
-    for (int m = 0; m < kMats; ++m)
-#pragma unroll
-      for (int i = 0; i < kR; ++i) {
-        p[m][i] = v[0][m][i];
-#pragma unroll
-        for (int k = 1; k < kS; ++k) p[m][i] += v[k][m][i];
-      }
-    gemm16_emit<kGated, kF16>(a, n, ti.row0 + c, nv, b0[0], b1[0], r[0], p[0], p[kMats - 1]);
-    if (kSides == 2)
-      gemm16_emit<false, kF16>(a, n + 128, ti.row0 + c, nv, b0[kSides - 1], 0.f, r[kSides - 1], p[1], p[1]);
+      for (int k = 1; k < kS; ++k) t.x += v[k][m].x, t.y += v[k][m].y, t.z += v[k][m].z, t.w += v[k][m].w;
+      p[m][0] = t.x, p[m][1] = t.y, p[m][2] = t.z, p[m][3] = t.w;
+    }
+    gemm16_emit4<kGated, kF16>(a, ti.n0 + 4 * lane, ti.row0 + c, p[0], p[kMats - 1]);
+    if (kMats == 2 && !kGated) gemm16_emit4<false, kF16>(a, ti.n0 + 128 + 4 * lane, ti.row0 + c, p[1], p[1]);
   }
 }
 
@@ -250,6 +290,11 @@ __global__ void __launch_bounds__(kG16Threads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(tmem_base_s, 2 * C::kAccCols);
+  if (tid == 0) {
+    tma_prefetch_map(&w_map);
+    tma_prefetch_map(&x64_map);
+    tma_prefetch_map(&x16_map);
+  }
   grid_dep_wait();
   if (kGrouped && warp == 2) {  // chunk table: exclusive scan of the experts' chunk counts
     int carry = 0;
@@ -457,6 +502,37 @@ inline bool device_info(DeviceInfo *d) {
   }
   if (e != cudaSuccess) set_cuda_error(e);
   return e == cudaSuccess;
+}
+
+// How many clusters of `splits` CTAs the device holds at once (looked up once
+// per device and size; every configuration has the same threads and all but
+// the same shared memory).
+template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16>
+int gemm16_clusters(int splits, int dev) {
+  using C = Gemm16Cfg<kMats, kNT>;
+  static std::atomic<int> most[64][4];
+  const int i = splits == 8 ? 3 : splits == 4 ? 2 : 1;
+  int n = most[dev][i].load(std::memory_order_acquire);
+  if (n == 0) {
+    auto kern = gemm16_kernel<kGrouped, kGated, kMats, kNT, kF16>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)splits);
+    cfg.blockDim = dim3(kG16Threads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();  // (not an error of the call: it runs without clusters)
+      n = -1;
+    }
+    most[dev][i].store(n, std::memory_order_release);
+  }
+  return n < 0 ? 0 : n;
 }
 
 template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16>

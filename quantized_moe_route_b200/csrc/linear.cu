@@ -31,6 +31,36 @@ static moe_status linear_stream(const Gemm16Args &g, const void *x, int64_t ldx,
              : linear_stream_launch<kGated, kF16, 1>(a, grid, wm, xm, d.dev, s);
 }
 
+// The rows of a tile and the CTAs that share its K: the least of a model of
+// the time in us, fitted to a sweep of both over N 512 to 8192, K 512 to 8192
+// and T 32 to 1024 (within 10 % of the sweep's best at most sizes).  A CTA
+// loads 94 KB/us, a k block's products take 0.16 us a block of weights (0.26
+// above 128 rows), joining a cluster's partials 0.4 us and 8 ns a row, and an
+// epilogue that nothing overlaps 5 ns a row.  (2048 x 2048, 256 rows: one chunk
+// over 8 CTAs 20.3 us, two over 4 each 8.8, eight whole ones 11.6.)
+template <bool kGated, bool kF16>
+static void gemm16_plan(Gemm16Args &a, const DeviceInfo &d) {
+  constexpr int kMats = kGated ? 2 : 1, kNT = kGated ? 128 : 256;
+  const int KB = (a.K + kG16BK - 1) / kG16BK;
+  const int most = gemm16_clusters<false, kGated, kMats, kNT, kF16>(8, d.dev) * 8 >= 64 ? 8 : 4;
+  float best = 1e30f;
+  for (int nt = min(kNT, (a.rows + 15) / 16 * 16); nt >= 16; nt -= 16) {
+    const int chunks = (a.rows + nt - 1) / nt;
+    if (chunks > 1 && nt > ((a.rows + chunks - 1) / chunks + 15) / 16 * 16) continue;  // a smaller nt has as few chunks
+    const int64_t tiles = (int64_t)a.nfb * chunks;
+    for (int S = 1; S <= most && (S == 1 || S * 2 <= KB); S *= 2) {
+      if (S > 1 && tiles > gemm16_clusters<false, kGated, kMats, kNT, kF16>(S, d.dev)) break;
+      const float kb = (float)((KB + S - 1) / S);
+      const float load = kb * (128 * kMats + nt) * (128.f / 94e3f), mma = kb * kMats * (nt > 128 ? 0.26f : 0.16f);
+      const int64_t waves = (tiles * S + d.sms - 1) / d.sms;
+      const float t = (float)waves * (load > mma ? load : mma) +
+                      (S > 1 ? 0.4f + 0.008f * nt * kMats : 0.005f * nt * kMats);
+      if (t < best) best = t, a.nt = nt, a.splits = S;
+    }
+    if (best < 1e30f && tiles > d.sms) break;  // finer tiles only add waves
+  }
+}
+
 template <bool kGated, bool kF16>
 static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const void *w, int64_t ldw, cudaStream_t s) {
   // gated: gate and up of 128 features and 128 rows a tile; else 128 outputs and 256 rows
@@ -45,13 +75,8 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
   }
   a.mat_off = a.N;
   a.nfb = (a.N + 127) / 128;
-  // equal chunks of rows
-  const int chunks = (a.rows + kNT - 1) / kNT;
-  a.nt = ((a.rows + chunks - 1) / chunks + 15) / 16 * 16;
+  gemm16_plan<kGated, kF16>(a, d);
   const int64_t tiles = (int64_t)a.nfb * ((a.rows + a.nt - 1) / a.nt);
-  const int KB = (a.K + kG16BK - 1) / kG16BK;
-  a.splits = 1;
-  while (a.splits < 8 && tiles * a.splits * 2 <= d.sms && a.splits * 4 <= KB) a.splits *= 2;
   const int grid = a.splits > 1 ? (int)tiles * a.splits : (int)(tiles < d.sms ? tiles : d.sms);
   return gemm16_launch<false, kGated, kMats, kNT, kF16>(a, grid, wm, x64, x16, d.dev, s);
 }

@@ -61,6 +61,10 @@ __global__ void __launch_bounds__(kLsWarps * 32, 1)
     for (int s = 0; s < kLsStages; ++s) mbar_init(&bars[s], 1);
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) {
+    tma_prefetch_map(&w_map);
+    tma_prefetch_map(&x_map);
+  }
   __syncwarp();
   grid_dep_wait();
   grid_dep_trigger();
