@@ -14,6 +14,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
@@ -24,8 +26,11 @@ MOE_DEVERR_DECODE_ROUTER_WAIT = 0x102
 MOE_W4_PLAIN, MOE_W4_GATE_UP = 0, 1
 MOE_BF16, MOE_F32, MOE_F16 = 0, 1, 2
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_SIGMOID = range(6)
+_TYPES = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_F16}
 
 _lib = None
+_call = None      # the C helper's call(address, *args)
+_address = {}     # entry points called through it
 
 
 class MoeError(RuntimeError):
@@ -114,7 +119,7 @@ SIGNATURES = {
 
 def lib():
     """The loaded libmoe (raises if the in-tree build is missing)."""
-    global _lib
+    global _lib, _call
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"libmoe.so is not built ({LIB_PATH}); run quantized_moe_route_b200/build.py")
@@ -123,6 +128,10 @@ def lib():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
+        from ._call import call
+        for name in ("moe_linear", "moe_decode_layer_bf16", "moe_ffn_grouped_prefill_bf16"):
+            _address[name] = ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+        _call = call
         _lib = L
     return _lib
 
@@ -372,56 +381,80 @@ def _refuse(why):
     raise MoeError(MOE_ERR_INVALID_ARG, why)
 
 
-def _ld(t, rows, cols):
-    """Row stride in elements of a [rows][cols] tensor whose rows are contiguous.  A single row has no next
-    one: any stride that the call accepts will do."""
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        _refuse("row elements must be contiguous")
-    return ld if rows > 1 else (cols + 7) // 8 * 8
+def _run(name, *args):
+    """Enqueues an entry point whose arguments are integers, addresses or None."""
+    if _lib is None:
+        lib()
+    status = _call(_address[name], *args)
+    if status != MOE_OK:
+        raise MoeError(status, name)
 
 
 def _here(*tensors):
-    """The tensors live on the current CUDA device, the one whose stream the call is enqueued on."""
-    import torch
+    """The current CUDA device, on which all of the tensors have to live (the call is enqueued there)."""
     dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2  # -1: a CPU tensor
     for t in tensors:
         if t is not None and t.get_device() != dev:
             _refuse("tensors must be on the current CUDA device")
+    return dev
+
+
+def _whole(*tensors):
+    """(tensor or None, bytes) pairs: each contiguous, of that many bytes, on the current CUDA device (returned)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    for t, nbytes in tensors:
+        if t is not None and (t.get_device() != dev or t.nbytes != nbytes or not t.is_contiguous()):
+            _refuse("a tensor of another size, not contiguous, or not on the current CUDA device")
+    return dev
+
+
+def _on(stream, dev):
+    """The stream's handle; None: the device's current stream (building a Stream object for it costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False, stream=None):
     """y [T][N] = act(x w^T + bias) + residual, or with gated (w [2N][K], gate rows first) act(g) * u + residual.
     x [T][K], w, bias and residual are bf16 (or int16 bits) or f16; y is of the same type or fp32.  Tensors may
     be rows of wider buffers (row strides of x and w in multiples of 8 elements)."""
-    import torch
     T, K = x.shape
     Ty, N = y.shape
     rows = 2 * N if gated else N
     dtype, ydtype = x.dtype, y.dtype
-    if w.shape != (rows, K) or Ty != T or w.dtype != dtype or x.element_size() != 2:
+    dt = _TYPES.get(dtype, -1)
+    if w.shape != (rows, K) or Ty != T or w.dtype != dtype or dt < 0:
         _refuse("moe_linear: shapes or types of x, w and y")
-    dt = MOE_F16 if dtype == torch.float16 else MOE_BF16
-    if ydtype == dtype:
-        ydt = dt
-    elif ydtype == torch.float32:
-        ydt = MOE_F32
-    else:
-        _refuse("moe_linear: type of y")
-    bp, rp, ldr = None, None, 0
+    ydt = dt if ydtype == dtype else MOE_F32 if ydtype == torch.float32 else -1
+    # rows of contiguous elements; a single row has no next one, so any stride that the call accepts will do
+    ldx, sx = x.stride()
+    ldw, sw = w.stride()
+    ldy, sy = y.stride()
+    if ydt < 0 or (sx != 1 and K > 1) or (sw != 1 and K > 1) or (sy != 1 and N > 1):
+        _refuse("moe_linear: type of y, or a row whose elements are not contiguous")
+    if T <= 1:
+        ldx, ldy = (K + 7) // 8 * 8, N
+    if rows <= 1:
+        ldw = (K + 7) // 8 * 8
+    bp = rp = None
+    ldr = 0
     if bias is not None:
         if bias.shape != (rows,) or bias.dtype != dtype or not bias.is_contiguous():
             _refuse("moe_linear: bias")
         bp = bias.data_ptr()
     if residual is not None:
-        if residual.shape != y.shape or residual.dtype != dtype:
+        ldr, sr = residual.stride()
+        if residual.shape != (T, N) or residual.dtype != dtype or (sr != 1 and N > 1):
             _refuse("moe_linear: residual")
-        rp, ldr = residual.data_ptr(), _ld(residual, T, N)
-    _here(x, w, y, bias, residual)
-    status = (_lib or lib()).moe_linear(x.data_ptr(), _ld(x, T, K), w.data_ptr(), _ld(w, rows, K), T, N, K, dt, bp, act,
-                                        1 if gated else 0, rp, ldr, y.data_ptr(), _ld(y, T, N), ydt, _stream(stream))
-    if status != MOE_OK:
-        raise MoeError(status, "moe_linear")
+        if T <= 1:
+            ldr = N
+        rp = residual.data_ptr()
+    dev = _here(x, w, y, bias, residual)
+    _run("moe_linear", x.data_ptr(), ldx, w.data_ptr(), ldw, T, N, K, dt, bp, act, 1 if gated else 0, rp, ldr,
+         y.data_ptr(), ldy, ydt, _on(stream, dev))
 
 
 def make_bf16_layer(E, H, F, gate_up, down) -> moe_bf16_layer:
@@ -437,11 +470,14 @@ def moe_decode_layer_bf16(layer: moe_bf16_layer, x, k, y, ws, wr=None, logits=No
                           residual=None, idx=None, w=None, stream=None):
     """One layer with bf16 experts: the router (from wr, or logits as given), routing, expert FFN, the optional
     shared expert (with its sigmoid gate), combine, residual."""
-    _here(x, wr, logits, y, ws, shared_gate, residual, idx, w)
-    T = x.shape[0]
-    _check(lib().moe_decode_layer_bf16(ctypes.byref(layer), _p(x), _p(wr), _p(logits), T, k, shared, _p(shared_gate),
-                                       _p(residual), _p(y), _p(idx), _p(w), _p(ws), ws.numel() * ws.element_size(),
-                                       _stream(stream)), "moe_decode_layer_bf16")
+    T, H = x.shape
+    Er = layer.E - shared
+    if H != layer.H:
+        _refuse("moe_decode_layer_bf16: x")
+    dev = _whole((x, 2 * T * H), (y, 2 * T * H), (wr, 2 * Er * H), (logits, 4 * T * Er), (shared_gate, 2 * H),
+                 (residual, 2 * T * H), (idx, 4 * T * k), (w, 4 * T * k), (ws, ws.nbytes))
+    _run("moe_decode_layer_bf16", ctypes.addressof(layer), x.data_ptr(), _ptr(wr), _ptr(logits), T, k, shared,
+         _ptr(shared_gate), _ptr(residual), y.data_ptr(), _ptr(idx), _ptr(w), ws.data_ptr(), ws.nbytes, _on(stream, dev))
 
 
 def moe_prefill_bf16_workspace_bytes(rows, F) -> int:
@@ -449,11 +485,13 @@ def moe_prefill_bf16_workspace_bytes(rows, F) -> int:
 
 
 def moe_ffn_grouped_prefill_bf16(layer: moe_bf16_layer, x_perm, offsets, y_perm, ws, stream=None):
-    _here(x_perm, offsets, y_perm, ws)
-    rows = x_perm.shape[0]
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().moe_ffn_grouped_prefill_bf16(ctypes.byref(layer), _p(x_perm), _p(offsets), rows, _p(y_perm), _p(ws),
-                                              nbytes, _stream(stream)), "moe_ffn_grouped_prefill_bf16")
+    rows, H = x_perm.shape
+    if H != layer.H:
+        _refuse("moe_ffn_grouped_prefill_bf16: x_perm")
+    dev = _whole((x_perm, 2 * rows * H), (y_perm, 2 * rows * H), (offsets, 4 * (layer.E + 1)),
+                 (ws, 0 if ws is None else ws.nbytes))
+    _run("moe_ffn_grouped_prefill_bf16", ctypes.addressof(layer), x_perm.data_ptr(), offsets.data_ptr(), rows,
+         y_perm.data_ptr(), _ptr(ws), 0 if ws is None else ws.nbytes, _on(stream, dev))
 
 
 def moe_device_error(stream=None) -> int:

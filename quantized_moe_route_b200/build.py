@@ -1,14 +1,16 @@
-"""Build libmoe.so (all CUDA sources of the C ABI) in-tree for sm_100a."""
+"""Build libmoe.so (all CUDA sources of the C ABI) in-tree for sm_100a, and the binding's call helper."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
+CALL_SRC, CALL_LIB = os.path.join(HERE, "_call.c"), os.path.join(HERE, "_call.so")
 ROOT = os.path.dirname(HERE)
 
 NVCC_FLAGS = [
@@ -34,7 +36,18 @@ def needs_build() -> bool:
     return any(os.path.getmtime(p) > t for p in sources() + headers())
 
 
+def build_call(force: bool = False) -> str:
+    """The C helper of the Python binding (gcc)."""
+    if force or not os.path.exists(CALL_LIB) or os.path.getmtime(CALL_LIB) < os.path.getmtime(CALL_SRC):
+        tmp = CALL_LIB + f".tmp{os.getpid()}"
+        subprocess.check_call(["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+                               "-o", tmp, CALL_SRC])
+        os.replace(tmp, CALL_LIB)
+    return CALL_LIB
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_call(force)
     if not force and not needs_build():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")

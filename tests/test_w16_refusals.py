@@ -117,3 +117,20 @@ def test_bf16_bindings_refuse_cpu_tensors():
     with pytest.raises(moe.MoeError) as ei:
         moe.moe_ffn_grouped_prefill_bf16(layer, x, torch.zeros(9, dtype=torch.int32), y, ws)
     assert ei.value.status == INV
+
+
+def test_bf16_bindings_refuse_other_sizes_types_and_strides():
+    """Everything a call would read or write past: sizes and types of every tensor, and views with gaps."""
+    bf = torch.bfloat16
+    layer = moe.moe_bf16_layer(8, 128, 64, P, P)
+    ok = dict(x=torch.zeros(2, 128, dtype=bf), y=torch.zeros(2, 128, dtype=bf), logits=torch.zeros(2, 8),
+              idx=torch.zeros(2, 2, dtype=torch.int32), w=torch.zeros(2, 2))
+    bad = [dict(x=torch.zeros(2, 64, dtype=bf)), dict(x=torch.zeros(2, 128)), dict(y=torch.zeros(1, 128, dtype=bf)),
+           dict(y=torch.zeros(2, 256, dtype=bf)[:, :128]), dict(logits=torch.zeros(2, 7)), dict(idx=torch.zeros(2, 2).long()),
+           dict(w=torch.zeros(2, 3)), dict(residual=torch.zeros(2, 64, dtype=bf)), dict(wr=torch.zeros(7, 128, dtype=bf))]
+    for kw in bad:
+        a = dict(ok)
+        a.update(kw)
+        with pytest.raises(moe.MoeError) as ei:
+            moe.moe_decode_layer_bf16(layer, a.pop("x"), 2, a.pop("y"), torch.zeros(1 << 16, dtype=torch.uint8), **a)
+        assert ei.value.status == INV, kw
