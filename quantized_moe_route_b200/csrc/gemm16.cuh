@@ -11,6 +11,15 @@
 // share the chunk's operand: gate and up of 128 features, or 256 consecutive
 // outputs, or (kMats = 1, kNT = 256) 128 outputs.
 //
+// Grouped, a tile holds at most 128 rows, and one of more than `flip` rows is
+// issued the other way round: the rows are M, the tile's two weight blocks one
+// N = 256 operand, and a lane of tensor memory is a row.  An MMA of M = 128, K =
+// 16 takes about 111 cycles for any N up to 200 and about 135 for 256, so
+// that is one product of 256 for two of up to 128, but it multiplies 128 rows
+// whatever is valid, and a long run of these kernels is held by the board's
+// power.  With flip = 32 the skewed prompt of 2048 tokens over 256 experts
+// takes 246 us (0: 258, 128: 258), one of 100 tokens 253 (0: 267, 128: 253).
+
 // Warp 0 loads 64-channel stages by TMA (128-byte swizzle; out-of-range rows
 // and channels arrive as zeros), warp 1 issues tcgen05.mma into one of two
 // accumulator sets in tensor memory, warps 2-13 run the epilogue of the other
@@ -38,6 +47,7 @@ struct Gemm16Args {
   int mat_off;             // weight rows from a tile's block 0 to its block 1
   int nfb;                 // output blocks per row chunk
   int nt;                  // rows per chunk (at most kNT, a multiple of 16)
+  int flip;                // grouped: tiles of more rows are issued with the rows on M
   int splits;              // CTAs of a cluster that share a tile (1: none, persistent over tiles)
   const uint16_t *bias, *residual;
   void *y;
@@ -265,6 +275,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
                   const __grid_constant__ CUtensorMap x16_map) {
   using C = Gemm16Cfg<kMats, kNT>;
   static_assert(!kGated || kMats == 2, "gate and up");
+  static_assert(!kGrouped || (kMats == 2 && kNT == 128), "rows on M, two weight blocks on N");
   constexpr int kOut = kGated ? 128 : 128 * kMats;  // outputs per tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (keeps the address space known)
@@ -362,7 +373,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
       uint32_t it = 0, tc = 0;
       for (int t = t0; t < ntiles && !*abort_s; t += G, ++tc) {
         const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
-        const uint32_t idesc = idesc_16_f32((ti.nvalid + 15) & ~15, kF16);
+        const uint32_t idesc = idesc_16_f32(kGrouped && ti.nvalid > a.flip ? 256 : (ti.nvalid + 15) & ~15, kF16);
         const uint32_t acc = tmem + (tc & 1u) * C::kAccCols;
         if (!mbar_wait_sleep(&acc_empty[tc & 1u], ((tc >> 1) & 1u) ^ 1u, kG16WaitPolls)) {
           fail();
@@ -379,6 +390,11 @@ __global__ void __launch_bounds__(kG16Threads, 1)
           }
           tc_fence_after();
           const uint64_t ad = desc0 + ((uint32_t)s * C::kStage >> 4), bd = ad + (C::kABytes >> 4);
+          if (kGrouped && ti.nvalid > a.flip) {
+#pragma unroll
+            for (int kk = 0; kk < kG16BK / 16; ++kk)
+              tc_mma_bf16(acc, bd + (kk * 32 >> 4), ad + (kk * 32 >> 4), idesc, (kb > kb0 || kk) ? 1u : 0u);
+          } else
 #pragma unroll
           for (int m = 0; m < kMats; ++m)
 #pragma unroll
@@ -416,6 +432,34 @@ __global__ void __launch_bounds__(kG16Threads, 1)
       }
       tc_fence_after();
       const uint32_t acc = tmem + (tc & 1u) * C::kAccCols + ((uint32_t)(q * 32) << 16);
+      if (kGrouped && ti.nvalid > a.flip) {
+        // lane: row 32 q + lane; columns: the tile's outputs (gated: gate, then up)
+        const int row = q * 32 + lane;
+        uint16_t *yr = static_cast<uint16_t *>(a.y) + (int64_t)(ti.row0 + row) * a.ldy + ti.n0;
+        if (q * 32 < ti.nvalid)
+          for (int c0 = sub * 16; c0 < min(kOut, a.N - ti.n0); c0 += kStep) {
+            uint32_t v[2][16], o[8];
+            tmem_ld16_async(acc + c0, v[0]);
+            if (kGated) tmem_ld16_async(acc + 128 + c0, v[1]);
+            tmem_ld_wait();
+            tmem_regs_after_wait(v[0]);
+            if (kGated) tmem_regs_after_wait(v[1]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float f[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                f[j] = __uint_as_float(v[0][2 * i + j]);
+                if (kGated) f[j] = activate(f[j], MOE_ACT_SILU) * __uint_as_float(v[1][2 * i + j]);
+              }
+              o[i] = cvt_bf16x2(f[0], f[1]);
+            }
+            if (row < ti.nvalid) {  // outputs in multiples of 16 on 32-byte boundaries of the row
+              *reinterpret_cast<uint4 *>(yr + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4 *>(yr + c0 + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          }
+      } else
       for (int c0 = sub * 16; c0 < ti.nvalid; c0 += kStep) {
         uint32_t v[kMats][16];
 #pragma unroll

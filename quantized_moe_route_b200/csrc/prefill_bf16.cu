@@ -48,6 +48,10 @@ extern "C" MOE_API moe_status moe_ffn_grouped_prefill_bf16(const moe_bf16_layer 
   a.w_rows = 2 * F;
   a.mat_off = F;
   a.nfb = (F + 127) / 128;
+  // a tile to an SM at most: latency counts, and the rows' own epilogue (16
+  // outputs a lane) is the shorter one (8 experts, 37 tokens: 11.7 against 14.9 us)
+  auto flip = [&]() { return ((int64_t)E + rows / 128) * a.nfb <= d.sms ? 0 : 32; };
+  a.flip = flip();
   a.y = h;
   a.ldy = F;
   a.act = MOE_ACT_SILU;
@@ -58,6 +62,7 @@ extern "C" MOE_API moe_status moe_ffn_grouped_prefill_bf16(const moe_bf16_layer 
   a.w_rows = H;
   a.mat_off = 128;
   a.nfb = (H + 255) / 256;
+  a.flip = flip();
   a.y = y_perm;
   a.ldy = H;
   a.act = MOE_ACT_NONE;
