@@ -47,7 +47,7 @@ struct Gemm16Args {
   int mat_off;             // weight rows from a tile's block 0 to its block 1
   int nfb;                 // output blocks per row chunk
   int nt;                  // rows per chunk (at most kNT, a multiple of 16)
-  int flip;                // grouped: tiles of more rows are issued with the rows on M
+  int flip;                // tiles of more rows are issued with the rows on M (two blocks of up to 128 rows)
   int splits;              // CTAs of a cluster that share a tile (1: none, persistent over tiles)
   const uint16_t *bias, *residual;
   void *y;
@@ -151,23 +151,25 @@ __device__ __forceinline__ void gemm16_residual(const Gemm16Args &a, int n, int6
 
 // kN rows of output n from their products p0 (and, gated, p1) and residual r:
 // bias (b0, b1), activation, gate, residual, store.
-template <bool kGated, bool kF16, int kN>
+template <bool kGated, bool kF16, int kN, bool kBare = false>
 __device__ __forceinline__ void gemm16_emit(const Gemm16Args &a, int n, int64_t row0, int nv, float b0, float b1,
                                             const uint16_t (&r)[kN], float (&p0)[kN], float (&p1)[kN]) {
   if (n >= a.N) return;
+  if (!kBare) {
 #pragma unroll
-  for (int i = 0; i < kN; ++i) p0[i] += b0;
-  activate_all(p0, a.act);
+    for (int i = 0; i < kN; ++i) p0[i] += b0;
+    activate_all(p0, a.act);
+  }
   if (kGated) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) p0[i] *= p1[i] + b1;
+    for (int i = 0; i < kN; ++i) p0[i] = (kBare ? activate(p0[i], MOE_ACT_SILU) : p0[i]) * (kBare ? p1[i] : p1[i] + b1);
   }
-  if (a.residual) {
+  if (!kBare && a.residual) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) p0[i] += w16_to_f32<kF16>(r[i]);
   }
   const int64_t o = row0 * a.ldy + n;
-  if (a.y_f32) {
+  if (!kBare && a.y_f32) {
     float *y = static_cast<float *>(a.y) + o;
 #pragma unroll
     for (int i = 0; i < kN; ++i)
@@ -242,6 +244,92 @@ __device__ __forceinline__ void gemm16_emit4(const Gemm16Args &a, int n, int64_t
   }
 }
 
+// Sixteen consecutive 16-bit values of a row (those below nv), as stored, in two
+// vectors where they lie on a 16-byte boundary.
+__device__ __forceinline__ void gemm16_load16(const uint16_t *p, int nv, uint32_t (&v)[8]) {
+  if (nv >= 16 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = (2 * i < nv ? p[2 * i] : 0u) | (2 * i + 1 < nv ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+  }
+}
+template <bool kF16>
+__device__ __forceinline__ float gemm16_half(uint32_t v, int hi) {
+  if (kF16) return w16_to_f32<true>((uint16_t)(v >> (16 * hi)));
+  return __uint_as_float(hi ? v & 0xFFFF0000u : v << 16);
+}
+
+// Sixteen consecutive outputs n .. n + 15 (those below a.N) of row `row`, from
+// their products and the row's residual: as gemm16_emit.  kBare: the grouped
+// FFN's, SiLU on the gate or nothing, bf16 outputs in whole vectors (a kernel's
+// first pass over its code is a walk through the instruction cache: with the
+// linear's epilogue in its place a small prompt takes 3 us more).
+template <bool kGated, bool kF16, bool kBare>
+__device__ __forceinline__ void gemm16_emit_row(const Gemm16Args &a, int n, int64_t row, const uint32_t (&r)[8],
+                                                float (&p0)[16], float (&p1)[16]) {
+  const int nv = a.N - n;
+  if (kBare) {
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float f0 = kGated ? activate(p0[2 * i], MOE_ACT_SILU) * p1[2 * i] : p0[2 * i];
+      const float f1 = kGated ? activate(p0[2 * i + 1], MOE_ACT_SILU) * p1[2 * i + 1] : p0[2 * i + 1];
+      o[i] = cvt_bf16x2(f0, f1);
+    }
+    uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.ldy + n;
+    reinterpret_cast<uint4 *>(y)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4 *>(y)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    return;
+  }
+  if (a.bias) {
+    uint32_t b[8];
+    gemm16_load16(a.bias + n, nv, b);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p0[i] += gemm16_half<kF16>(b[i >> 1], i & 1);
+  }
+  activate_all(p0, a.act);
+  if (kGated) {
+    uint32_t b[8] = {};
+    if (a.bias) gemm16_load16(a.bias + a.N + n, nv, b);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p0[i] *= p1[i] + gemm16_half<kF16>(b[i >> 1], i & 1);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) p0[i] += gemm16_half<kF16>(r[i >> 1], i & 1);
+  }
+  if (a.y_f32) {
+    float *y = static_cast<float *>(a.y) + row * a.ldy + n;
+    if (nv >= 16 && reinterpret_cast<uintptr_t>(y) % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<float4 *>(y)[i] = make_float4(p0[4 * i], p0[4 * i + 1], p0[4 * i + 2], p0[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < nv) y[i] = p0[i];
+    }
+  } else {
+    uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.ldy + n;
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      o[i] = kF16 ? (uint32_t)f32_to_w16<true>(p0[2 * i]) | (uint32_t)f32_to_w16<true>(p0[2 * i + 1]) << 16
+                  : cvt_bf16x2(p0[2 * i], p0[2 * i + 1]);
+    if (nv >= 16 && reinterpret_cast<uintptr_t>(y) % 16 == 0) {
+      reinterpret_cast<uint4 *>(y)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      reinterpret_cast<uint4 *>(y)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < nv) y[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
 // A cluster's epilogue: CTA `rank` of kS adds up its share of the tile's rows
 // over the partials of all kS CTAs, in rank order: a warp takes a row, a lane
 // four of its 128 outputs, with the loads from all CTAs in flight together.
@@ -275,7 +363,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
                   const __grid_constant__ CUtensorMap x16_map) {
   using C = Gemm16Cfg<kMats, kNT>;
   static_assert(!kGated || kMats == 2, "gate and up");
-  static_assert(!kGrouped || (kMats == 2 && kNT == 128), "rows on M, two weight blocks on N");
+  constexpr bool kCanFlip = kMats == 2 && kNT == 128;  // rows on M, two weight blocks on N
   constexpr int kOut = kGated ? 128 : 128 * kMats;  // outputs per tile
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (keeps the address space known)
@@ -331,7 +419,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
   const uint32_t tmem = *tmem_base_s;
   const int nchunks = kGrouped ? start[a.E] : (a.rows + a.nt - 1) / a.nt;
   const int ntiles = nchunks * a.nfb;
-  const int S = a.splits, rank = S > 1 ? (int)cluster_rank() : 0;
+  const int S = kGrouped ? 1 : a.splits, rank = S > 1 ? (int)cluster_rank() : 0;
   const int t0 = blockIdx.x / S, G = gridDim.x / S;
   const int KB = (a.K + kG16BK - 1) / kG16BK;
   const int kb0 = KB * rank / S, kb1 = KB * (rank + 1) / S;  // S <= KB: never empty
@@ -373,7 +461,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
       uint32_t it = 0, tc = 0;
       for (int t = t0; t < ntiles && !*abort_s; t += G, ++tc) {
         const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
-        const uint32_t idesc = idesc_16_f32(kGrouped && ti.nvalid > a.flip ? 256 : (ti.nvalid + 15) & ~15, kF16);
+        const uint32_t idesc = idesc_16_f32(kCanFlip && ti.nvalid > a.flip ? 256 : (ti.nvalid + 15) & ~15, kF16);
         const uint32_t acc = tmem + (tc & 1u) * C::kAccCols;
         if (!mbar_wait_sleep(&acc_empty[tc & 1u], ((tc >> 1) & 1u) ^ 1u, kG16WaitPolls)) {
           fail();
@@ -390,7 +478,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
           }
           tc_fence_after();
           const uint64_t ad = desc0 + ((uint32_t)s * C::kStage >> 4), bd = ad + (C::kABytes >> 4);
-          if (kGrouped && ti.nvalid > a.flip) {
+          if (kCanFlip && ti.nvalid > a.flip) {
 #pragma unroll
             for (int kk = 0; kk < kG16BK / 16; ++kk)
               tc_mma_bf16(acc, bd + (kk * 32 >> 4), ad + (kk * 32 >> 4), idesc, (kb > kb0 || kk) ? 1u : 0u);
@@ -417,9 +505,9 @@ __global__ void __launch_bounds__(kG16Threads, 1)
       const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
       const int n = ti.n0 + q * 32 + lane;
       constexpr int kSides = kMats == 2 && !kGated ? 2 : 1;  // outputs n and n + 128
-      float b0[kSides], b1[kSides];
+      float b0[kSides] = {}, b1[kSides] = {};
       uint16_t r[kSides][16] = {};
-      if (S == 1) {  // what does not depend on the products, before waiting for them
+      if (!kGrouped && S == 1 && !(kCanFlip && ti.nvalid > a.flip)) {  // what does not depend on the products, before waiting for them
 #pragma unroll
         for (int m = 0; m < kSides; ++m) {
           gemm16_bias<kGated, kF16>(a, n + 128 * m, b0[m], b1[m]);
@@ -432,40 +520,38 @@ __global__ void __launch_bounds__(kG16Threads, 1)
       }
       tc_fence_after();
       const uint32_t acc = tmem + (tc & 1u) * C::kAccCols + ((uint32_t)(q * 32) << 16);
-      if (kGrouped && ti.nvalid > a.flip) {
+      if (kCanFlip && ti.nvalid > a.flip) {
         // lane: row 32 q + lane; columns: the tile's outputs (gated: gate, then up)
-        const int row = q * 32 + lane;
-        uint16_t *yr = static_cast<uint16_t *>(a.y) + (int64_t)(ti.row0 + row) * a.ldy + ti.n0;
+        const int row = q * 32 + lane, outs = min(kOut, a.N - ti.n0);
+        const bool live = row < ti.nvalid;
+        const uint16_t *rrow = a.residual + (int64_t)(ti.row0 + row) * a.ldr + ti.n0;
+        uint32_t rr[8] = {};
+        if (!kGrouped && a.residual && live && sub * 16 < outs) gemm16_load16(rrow + sub * 16, outs - sub * 16, rr);
         if (q * 32 < ti.nvalid)
-          for (int c0 = sub * 16; c0 < min(kOut, a.N - ti.n0); c0 += kStep) {
-            uint32_t v[2][16], o[8];
+          for (int c0 = sub * 16; c0 < outs; c0 += kStep) {
+            uint32_t v[2][16], rnext[8] = {};
             tmem_ld16_async(acc + c0, v[0]);
             if (kGated) tmem_ld16_async(acc + 128 + c0, v[1]);
+            if (!kGrouped && a.residual && live && c0 + kStep < outs) gemm16_load16(rrow + c0 + kStep, outs - c0 - kStep, rnext);
             tmem_ld_wait();
-            tmem_regs_after_wait(v[0]);
-            if (kGated) tmem_regs_after_wait(v[1]);
+            float p[2][16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              float f[2];
+            for (int m = 0; m < (kGated ? 2 : 1); ++m) {
+              tmem_regs_after_wait(v[m]);
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                f[j] = __uint_as_float(v[0][2 * i + j]);
-                if (kGated) f[j] = activate(f[j], MOE_ACT_SILU) * __uint_as_float(v[1][2 * i + j]);
-              }
-              o[i] = cvt_bf16x2(f[0], f[1]);
+              for (int i = 0; i < 16; ++i) p[m][i] = __uint_as_float(v[m][i]);
             }
-            if (row < ti.nvalid) {  // outputs in multiples of 16 on 32-byte boundaries of the row
-              *reinterpret_cast<uint4 *>(yr + c0) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4 *>(yr + c0 + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
+            if (live) gemm16_emit_row<kGated, kF16, kGrouped>(a, ti.n0 + c0, ti.row0 + row, rr, p[0], p[kGated ? 1 : 0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rr[i] = rnext[i];
           }
       } else
       for (int c0 = sub * 16; c0 < ti.nvalid; c0 += kStep) {
         uint32_t v[kMats][16];
 #pragma unroll
         for (int m = 0; m < kMats; ++m) tmem_ld16_async(acc + m * kNT + c0, v[m]);
-        uint16_t rn[kSides][16];
-        if (a.residual && S == 1) {  // the next batch's
+        uint16_t rn[kSides][16] = {};
+        if (!kGrouped && a.residual && S == 1) {  // the next batch's
 #pragma unroll
           for (int m = 0; m < kSides; ++m)
             gemm16_residual(a, n + 128 * m, ti.row0 + c0 + kStep, ti.nvalid - c0 - kStep, rn[m]);
@@ -485,9 +571,9 @@ __global__ void __launch_bounds__(kG16Threads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) part[(m * kNT + c0 + i) * 128 + q * 32 + lane] = p[m][i];
         } else {
-          gemm16_emit<kGated, kF16>(a, n, ti.row0 + c0, ti.nvalid - c0, b0[0], b1[0], r[0], p[0], p[kMats - 1]);
+          gemm16_emit<kGated, kF16, 16, kGrouped>(a, n, ti.row0 + c0, ti.nvalid - c0, b0[0], b1[0], r[0], p[0], p[kMats - 1]);
           if (kSides == 2)
-            gemm16_emit<false, kF16>(a, n + 128, ti.row0 + c0, ti.nvalid - c0, b0[kSides - 1], 0.f, r[kSides - 1], p[1],
+            gemm16_emit<false, kF16, 16, kGrouped>(a, n + 128, ti.row0 + c0, ti.nvalid - c0, b0[kSides - 1], 0.f, r[kSides - 1], p[1],
                                      p[1]);
 #pragma unroll
           for (int m = 0; m < kSides; ++m)

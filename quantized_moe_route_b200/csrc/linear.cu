@@ -73,8 +73,22 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
     set_cuda_error(cudaErrorInvalidValue);
     return MOE_ERR_CUDA;
   }
+  // Enough tiles of 128 rows and two weight blocks (256 outputs, or gate and up
+  // of 128) for every SM: the rows go on M, and a lane of the epilogue holds 16
+  // outputs of a row, one vector, where the other way round it has one output
+  // of 16 rows.  (8192 x 8192 x 2048 with bias, GELU and residual: see above.)
+  const int64_t large = (int64_t)((a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256)) * ((a.rows + 127) / 128);
+  if (large >= d.sms) {
+    a.mat_off = kGated ? a.N : 128;
+    a.nfb = (a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256);
+    a.nt = 128;
+    a.splits = 1;
+    a.flip = 0;
+    return gemm16_launch<false, kGated, 2, 128, kF16>(a, d.sms, wm, x64, x16, d.dev, s);
+  }
   a.mat_off = a.N;
   a.nfb = (a.N + 127) / 128;
+  a.flip = 128;
   gemm16_plan<kGated, kF16>(a, d);
   const int64_t tiles = (int64_t)a.nfb * ((a.rows + a.nt - 1) / a.nt);
   const int grid = a.splits > 1 ? (int)tiles * a.splits : (int)(tiles < d.sms ? tiles : d.sms);
