@@ -574,10 +574,11 @@ typedef enum {
  * y may be the residual itself (same address, type and row stride); beyond
  * that no output may overlap an input.
  * Requirements: x and w 16-byte aligned, ldx % 8 == 0 and ldw % 8 == 0, N <=
- * 2^29, row strides up to 2^38; any T, N, K.  T == 0 or N == 0 is a no-op.
+ * 2^29, T and K <= 2^30, row strides up to 2^38; otherwise any T, N, K.  T == 0 or N == 0 is a no-op.
  * No workspace.  Errors: INVALID_ARG (null, a negative size, K == 0, an unknown type
- * or activation, a row stride below its row's length, misalignment),
- * UNSUPPORTED_SHAPE, CUDA.
+ * or activation, a row stride below its row's length, misalignment, y at x, w
+ * or bias), UNSUPPORTED_SHAPE, CUDA.  A wait on the device that runs out (it
+ * cannot in a sound call) raises MOE_DEVERR_PREFILL_WAIT.
  */
 MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, int T, int N,
                               int K, int dtype, const void *bias, int act, int gated,

@@ -743,7 +743,7 @@ extern "C" MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer,
     return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
   if (!layer->gate_up || !layer->down || !x || (!wr && !logits) || !y) return MOE_ERR_INVALID_ARG;
-  if ((idx == nullptr) != (w == nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((idx == nullptr) != (w == nullptr) || y == x) return MOE_ERR_INVALID_ARG;
   for (const void *p : {(const void *)layer->gate_up, (const void *)layer->down, (const void *)x, (const void *)wr,
                         (const void *)shared_gate, (const void *)residual, (const void *)y, (const void *)ws})
     if (reinterpret_cast<uintptr_t>(p) % 16) return MOE_ERR_INVALID_ARG;

@@ -109,14 +109,14 @@ extern "C" MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void 
   if (!x || !w || !y) return MOE_ERR_INVALID_ARG;
   if (ldx < K || ldw < K || ldy < N || (residual && ldr < N)) return MOE_ERR_INVALID_ARG;
   const int64_t ld_max = (int64_t)1 << 38;
-  if (ldx % 8 || ldw % 8 || ldx > ld_max || ldw > ld_max || ldy > ld_max || (residual && ldr > ld_max) || N > (1 << 29))
+  if (ldx % 8 || ldw % 8 || ldx > ld_max || ldw > ld_max || ldy > ld_max || (residual && ldr > ld_max) || N > (1 << 29) || T > (1 << 30) || K > (1 << 30))
     return MOE_ERR_UNSUPPORTED_SHAPE;
   const uintptr_t ymask = y_dtype == MOE_F32 ? 3 : 1;
   if (reinterpret_cast<uintptr_t>(x) % 16 || reinterpret_cast<uintptr_t>(w) % 16 ||
       (reinterpret_cast<uintptr_t>(y) & ymask) || reinterpret_cast<uintptr_t>(bias) % 2 ||
       reinterpret_cast<uintptr_t>(residual) % 2)
     return MOE_ERR_INVALID_ARG;
-  if (residual == y && (y_dtype == MOE_F32 || ldr != ldy)) return MOE_ERR_INVALID_ARG;
+  if (y == x || y == w || y == bias || (residual == y && (y_dtype == MOE_F32 || ldr != ldy))) return MOE_ERR_INVALID_ARG;
   Gemm16Args a = {};
   a.E = 1;
   a.rows = T;

@@ -253,3 +253,56 @@ def test_empty_calls_write_nothing():
     moe.moe_linear(x, w[:0], y[:, :0])
     torch.cuda.synchronize()
     assert (y == 9.0).all()
+
+
+def test_non_finite_rows_stay_in_their_rows():
+    """Infinities and NaN in a row of x, or of w, reach that row's (that output's) results and no others."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    for T, N, K in [(5, 40, 136), (13, 300, 520), (100, 300, 520), (700, 1024, 200)]:
+        x, w = ints(gen, (T, K), torch.bfloat16), ints(gen, (N, K), torch.bfloat16)
+        y0, y1 = torch.empty((T, N), device="cuda"), torch.empty((T, N), device="cuda")
+        moe.moe_linear(x, w, y0)
+        x[T // 2, 3], x[1, K - 1], w[N - 1, 0] = float("nan"), float("inf"), float("-inf")
+        moe.moe_linear(x, w, y1)
+        keep = torch.ones((T, N), dtype=torch.bool, device="cuda")
+        keep[T // 2], keep[1], keep[:, N - 1] = False, False, False
+        assert torch.equal(y0[keep], y1[keep])
+        assert torch.isnan(y1[T // 2]).all() and not torch.isfinite(y1[1][w[:, K - 1] != 0]).any()
+
+
+@pytest.mark.parametrize("which", ["linear", "decode", "grouped"])
+def test_first_call_of_a_process_inside_a_capture(which):
+    """Attributes, maps and occupancy are looked up on the first call, which may be a captured one."""
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import sys
+sys.path.insert(0, {os.path.dirname(os.path.dirname(os.path.abspath(__file__)))!r})
+import torch
+import quantized_moe_route_b200 as moe
+bf = torch.bfloat16
+gu, dn = torch.ones((4, 128, 64), dtype=bf, device="cuda") / 64, torch.ones((4, 64, 64), dtype=bf, device="cuda") / 64
+layer = moe.make_bf16_layer(4, 64, 64, gu, dn)
+x, y = torch.ones((40, 64), dtype=bf, device="cuda"), torch.zeros((40, 64), dtype=bf, device="cuda")
+off = torch.tensor([0, 10, 20, 30, 40], dtype=torch.int32, device="cuda")
+ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+lg = torch.zeros((4, 4), device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    if {which!r} == "linear":
+        moe.moe_linear(x, gu[0, :64], y)
+        moe.moe_linear(x[:4], gu[0, :64], y[:4])
+    elif {which!r} == "decode":
+        moe.moe_decode_layer_bf16(layer, x[:4], 2, y[:4], ws, logits=lg)
+    else:
+        moe.moe_ffn_grouped_prefill_bf16(layer, x, off, y, ws)
+g.replay()
+torch.cuda.synchronize()
+s = 1 / (1 + torch.tensor(-1.0).exp())  # g = u = 1, h = silu(1), y = h
+want = 1.0 if {which!r} == "linear" else s.item()
+assert (y[:4].float() - want).abs().max() < 0.01, y
+assert moe.moe_device_error() == 0
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)

@@ -9,11 +9,11 @@ import torch
 import quantized_moe_route_b200 as moe
 
 INV, SHAPE, WS = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED_SHAPE, moe.MOE_ERR_WORKSPACE
-P = 1 << 20  # an aligned address that is never followed
+P, Q = 1 << 20, 1 << 30  # aligned addresses that are never followed
 
 
 def linear(x=P, ldx=64, w=P, ldw=64, T=4, N=32, K=64, dtype=moe.MOE_BF16, bias=None, act=0, gated=0, residual=None,
-           ldr=0, y=P, ldy=32, y_dtype=None):
+           ldr=0, y=Q, ldy=32, y_dtype=None):
     y_dtype = dtype if y_dtype is None else y_dtype
     return moe.lib().moe_linear(x, ldx, w, ldw, T, N, K, dtype, bias, act, gated, residual, ldr, y, ldy, y_dtype, None)
 
@@ -25,10 +25,12 @@ def linear(x=P, ldx=64, w=P, ldw=64, T=4, N=32, K=64, dtype=moe.MOE_BF16, bias=N
     (INV, dict(gated=2)), (INV, dict(gated=-1)),
     (INV, dict(x=None)), (INV, dict(w=None)), (INV, dict(y=None)),
     (INV, dict(ldx=56)), (INV, dict(ldw=56)), (INV, dict(ldy=31)), (INV, dict(residual=P, ldr=31)),
-    (INV, dict(x=P + 8)), (INV, dict(w=P + 2)), (INV, dict(y=P + 1)), (INV, dict(y=P + 2, y_dtype=moe.MOE_F32)),
+    (INV, dict(x=P + 8)), (INV, dict(w=P + 2)), (INV, dict(y=Q + 1)), (INV, dict(y=Q + 2, y_dtype=moe.MOE_F32)),
     (INV, dict(bias=P + 1)), (INV, dict(residual=P + 1, ldr=32)),
-    (INV, dict(residual=P, ldr=40, ldy=32)), (INV, dict(residual=P, ldr=32, y_dtype=moe.MOE_F32)),
+    (INV, dict(residual=Q, ldr=40, ldy=32)), (INV, dict(residual=Q, ldr=32, y_dtype=moe.MOE_F32)),
+    (INV, dict(y=P)), (INV, dict(bias=Q)),
     (SHAPE, dict(ldx=68)), (SHAPE, dict(ldw=65)), (SHAPE, dict(ldx=(1 << 38) + 8)),
+    (SHAPE, dict(T=(1 << 30) + 1)), (SHAPE, dict(K=(1 << 30) + 1, ldx=1 << 31, ldw=1 << 31)),
     (SHAPE, dict(N=(1 << 29) + 1, ldy=1 << 31)),
     (moe.MOE_OK, dict(T=0)), (moe.MOE_OK, dict(N=0)), (moe.MOE_OK, dict(T=0, x=None, w=None, y=None)),
 ])
@@ -54,7 +56,7 @@ def test_linear_binding_refuses_what_the_abi_cannot_see():
         assert ei.value.status == INV, kw
 
 
-def decode(E=8, H=128, F=64, gu=P, dn=P, x=P, wr=P, logits=None, T=2, k=2, shared=0, sg=None, residual=None, y=P,
+def decode(E=8, H=128, F=64, gu=P, dn=P, x=P, wr=P, logits=None, T=2, k=2, shared=0, sg=None, residual=None, y=Q,
            idx=None, w=None, ws=P, ws_bytes=1 << 40):
     layer = moe.moe_bf16_layer(E, H, F, gu, dn)
     return moe.lib().moe_decode_layer_bf16(ctypes.byref(layer), x, wr, logits, T, k, shared, sg, residual, y, idx, w,
@@ -66,7 +68,7 @@ def decode(E=8, H=128, F=64, gu=P, dn=P, x=P, wr=P, logits=None, T=2, k=2, share
     (INV, dict(H=0)), (INV, dict(F=-64)), (INV, dict(k=9)), (INV, dict(k=8, shared=1)), (INV, dict(E=1, k=1, shared=1)),
     (INV, dict(sg=P)), (INV, dict(gu=None)), (INV, dict(dn=None)), (INV, dict(x=None)), (INV, dict(y=None)),
     (INV, dict(wr=None)), (INV, dict(idx=P)), (INV, dict(w=P)),
-    (INV, dict(gu=P + 8)), (INV, dict(dn=P + 8)), (INV, dict(x=P + 2)), (INV, dict(wr=P + 2)), (INV, dict(y=P + 4)),
+    (INV, dict(gu=P + 8)), (INV, dict(dn=P + 8)), (INV, dict(x=P + 2)), (INV, dict(wr=P + 2)), (INV, dict(y=Q + 4)), (INV, dict(y=P)),
     (INV, dict(residual=P + 2)), (INV, dict(shared=1, sg=P + 2)), (INV, dict(ws=P + 8)), (INV, dict(logits=P + 2)),
     (INV, dict(idx=P + 2, w=P)), (INV, dict(idx=P, w=P + 1)),
     (SHAPE, dict(H=96)), (SHAPE, dict(F=32)), (SHAPE, dict(T=17)), (SHAPE, dict(E=64, T=16, k=17)),
