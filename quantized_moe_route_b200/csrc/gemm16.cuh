@@ -35,6 +35,7 @@ namespace moe {
 
 constexpr int kG16BK = 64;
 constexpr int kG16Stages = 4;
+constexpr int kG16Seg = 8;          // k blocks that one accumulation runs over where y is fp32
 constexpr int kG16EpiWarps = 12;  // three to a lane quarter of tensor memory
 constexpr int kG16Threads = (2 + kG16EpiWarps) * 32;
 constexpr uint32_t kG16WaitPolls = 1u << 18;  // sleeping polls of up to 10 us: a bound of seconds
@@ -357,7 +358,7 @@ __device__ __forceinline__ void gemm16_join(const Gemm16Args &a, const Gemm16Til
   }
 }
 
-template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16>
+template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16, bool kSeg = false>
 __global__ void __launch_bounds__(kG16Threads, 1)
     gemm16_kernel(Gemm16Args a, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x64_map,
                   const __grid_constant__ CUtensorMap x16_map) {
@@ -459,40 +460,45 @@ __global__ void __launch_bounds__(kG16Threads, 1)
     if (lane == 0) {
       const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
       uint32_t it = 0, tc = 0;
-      for (int t = t0; t < ntiles && !*abort_s; t += G, ++tc) {
+      for (int t = t0; t < ntiles && !*abort_s; t += G) {
         const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
         const uint32_t idesc = idesc_16_f32(kCanFlip && ti.nvalid > a.flip ? 256 : (ti.nvalid + 15) & ~15, kF16);
-        const uint32_t acc = tmem + (tc & 1u) * C::kAccCols;
-        if (!mbar_wait_sleep(&acc_empty[tc & 1u], ((tc >> 1) & 1u) ^ 1u, kG16WaitPolls)) {
-          fail();
-          break;
-        }
-        tc_fence_after();
         bool ok = true;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % kG16Stages;
-          if (!mbar_wait_sleep(&full[s], (it / kG16Stages) & 1u, kG16WaitPolls)) {
+        for (int kb = kb0; kb < kb1 && ok; ++tc) {  // accumulations: one, or one a segment
+          const uint32_t acc = tmem + (tc & 1u) * C::kAccCols;
+          if (!mbar_wait_sleep(&acc_empty[tc & 1u], ((tc >> 1) & 1u) ^ 1u, kG16WaitPolls)) {
             fail();
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = desc0 + ((uint32_t)s * C::kStage >> 4), bd = ad + (C::kABytes >> 4);
-          if (kCanFlip && ti.nvalid > a.flip) {
+          const int first = kb, last = kSeg ? min(kb1, kb + kG16Seg) : kb1;
+          for (; kb < last; ++kb, ++it) {
+            const int s = it % kG16Stages;
+            if (!mbar_wait_sleep(&full[s], (it / kG16Stages) & 1u, kG16WaitPolls)) {
+              fail();
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = desc0 + ((uint32_t)s * C::kStage >> 4), bd = ad + (C::kABytes >> 4);
+            if (kCanFlip && ti.nvalid > a.flip) {
 #pragma unroll
-            for (int kk = 0; kk < kG16BK / 16; ++kk)
-              tc_mma_bf16(acc, bd + (kk * 32 >> 4), ad + (kk * 32 >> 4), idesc, (kb > kb0 || kk) ? 1u : 0u);
-          } else
+              for (int kk = 0; kk < kG16BK / 16; ++kk)
+                tc_mma_bf16(acc, bd + (kk * 32 >> 4), ad + (kk * 32 >> 4), idesc, (kb > first || kk) ? 1u : 0u);
+            } else {
 #pragma unroll
-          for (int m = 0; m < kMats; ++m)
+              for (int m = 0; m < kMats; ++m)
 #pragma unroll
-            for (int kk = 0; kk < kG16BK / 16; ++kk)
-              tc_mma_bf16(acc + m * kNT, ad + ((m * 128 * 128 + kk * 32) >> 4), bd + (kk * 32 >> 4), idesc,
-                          (kb > kb0 || kk) ? 1u : 0u);
-          tc_commit(&empty[s]);
+                for (int kk = 0; kk < kG16BK / 16; ++kk)
+                  tc_mma_bf16(acc + m * kNT, ad + ((m * 128 * 128 + kk * 32) >> 4), bd + (kk * 32 >> 4), idesc,
+                              (kb > first || kk) ? 1u : 0u);
+            }
+            tc_commit(&empty[s]);
+          }
+          if (ok) tc_commit(&acc_full[tc & 1u]);
         }
         if (!ok) break;
-        tc_commit(&acc_full[tc & 1u]);
       }
     }
   } else {
@@ -504,6 +510,60 @@ __global__ void __launch_bounds__(kG16Threads, 1)
     for (int t = t0; t < ntiles && !*abort_s; t += G, ++tc) {
       const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
       const int n = ti.n0 + q * 32 + lane;
+      if constexpr (kSeg) {
+        // The tensor core's fp32 additions truncate: after 128 steps of k a sum is
+        // 1.9e-6 too small, which a 16-bit result does not see and an fp32 one
+        // does.  So here an accumulation runs over 512 inputs, and the segments
+        // are added in registers (K = 2048: 4e-7).
+        static_assert(!kGrouped && !kCanFlip, "weights on M");
+        constexpr int kB = (kNT + kStep - 1) / kStep;
+        float sum[kB][kMats][16] = {};
+        bool ok = true;
+        for (int k0 = kb0; k0 < kb1; k0 += kG16Seg, ++tc) {
+          if (!mbar_wait_sleep(&acc_full[tc & 1u], (tc >> 1) & 1u, kG16WaitPolls)) {
+            fail();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t acc = tmem + (tc & 1u) * C::kAccCols + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+          for (int b = 0; b < kB; ++b) {
+            const int c0 = sub * 16 + b * kStep;
+            if (c0 >= ti.nvalid) break;
+#pragma unroll
+            for (int m = 0; m < kMats; ++m) {
+              uint32_t v[16];
+              tmem_ld16(acc + m * kNT + c0, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[b][m][i] += __uint_as_float(v[i]);
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&acc_empty[tc & 1u]);
+        }
+        --tc;  // (the loop counts accumulations)
+        if (!ok) break;
+        float b0 = 0.f, b1 = 0.f;
+        if (S == 1) gemm16_bias<kGated, kF16>(a, n, b0, b1);
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+          const int c0 = sub * 16 + b * kStep;
+          if (c0 >= ti.nvalid) break;
+          if (S > 1) {
+            float *part = reinterpret_cast<float *>(smem);
+#pragma unroll
+            for (int m = 0; m < kMats; ++m)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) part[(m * kNT + c0 + i) * 128 + q * 32 + lane] = sum[b][m][i];
+          } else {
+            uint16_t r[16] = {};
+            if (a.residual) gemm16_residual(a, n, ti.row0 + c0, ti.nvalid - c0, r);
+            gemm16_emit<kGated, kF16, 16>(a, n, ti.row0 + c0, ti.nvalid - c0, b0, b1, r, sum[b][0], sum[b][kMats - 1]);
+          }
+        }
+        continue;
+      }
       constexpr int kSides = kMats == 2 && !kGated ? 2 : 1;  // outputs n and n + 128
       float b0[kSides] = {}, b1[kSides] = {};
       uint16_t r[kSides][16] = {};
@@ -637,14 +697,14 @@ inline bool device_info(DeviceInfo *d) {
 // How many clusters of `splits` CTAs the device holds at once (looked up once
 // per device and size; every configuration has the same threads and all but
 // the same shared memory).
-template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16>
+template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16, bool kSeg = false>
 int gemm16_clusters(int splits, int dev) {
   using C = Gemm16Cfg<kMats, kNT>;
   static std::atomic<int> most[64][4];
   const int i = splits == 8 ? 3 : splits == 4 ? 2 : 1;
   int n = most[dev][i].load(std::memory_order_acquire);
   if (n == 0) {
-    auto kern = gemm16_kernel<kGrouped, kGated, kMats, kNT, kF16>;
+    auto kern = gemm16_kernel<kGrouped, kGated, kMats, kNT, kF16, kSeg>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)splits);
     cfg.blockDim = dim3(kG16Threads);
@@ -665,11 +725,11 @@ int gemm16_clusters(int splits, int dev) {
   return n < 0 ? 0 : n;
 }
 
-template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16>
+template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16, bool kSeg = false>
 moe_status gemm16_launch(const Gemm16Args &a, int grid, const CUtensorMap &w, const CUtensorMap &x64,
                          const CUtensorMap &x16, int dev, cudaStream_t stream) {
   using C = Gemm16Cfg<kMats, kNT>;
-  auto kern = gemm16_kernel<kGrouped, kGated, kMats, kNT, kF16>;
+  auto kern = gemm16_kernel<kGrouped, kGated, kMats, kNT, kF16, kSeg>;
   static std::atomic<bool> attr_done[64];  // per device; the attribute call is idempotent
   if (!attr_done[dev].load(std::memory_order_acquire)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);

@@ -38,18 +38,17 @@ static moe_status linear_stream(const Gemm16Args &g, const void *x, int64_t ldx,
 // above 128 rows), joining a cluster's partials 0.4 us and 8 ns a row, and an
 // epilogue that nothing overlaps 5 ns a row.  (2048 x 2048, 256 rows: one chunk
 // over 8 CTAs 20.3 us, two over 4 each 8.8, eight whole ones 11.6.)
-template <bool kGated, bool kF16>
+template <bool kGated, int kMats, int kNT, bool kF16, bool kSeg>
 static void gemm16_plan(Gemm16Args &a, const DeviceInfo &d) {
-  constexpr int kMats = kGated ? 2 : 1, kNT = kGated ? 128 : 256;
   const int KB = (a.K + kG16BK - 1) / kG16BK;
-  const int most = gemm16_clusters<false, kGated, kMats, kNT, kF16>(8, d.dev) * 8 >= 64 ? 8 : 4;
+  const int most = gemm16_clusters<false, kGated, kMats, kNT, kF16, kSeg>(8, d.dev) * 8 >= 64 ? 8 : 4;
   float best = 1e30f;
   for (int nt = min(kNT, (a.rows + 15) / 16 * 16); nt >= 16; nt -= 16) {
     const int chunks = (a.rows + nt - 1) / nt;
     if (chunks > 1 && nt > ((a.rows + chunks - 1) / chunks + 15) / 16 * 16) continue;  // a smaller nt has as few chunks
     const int64_t tiles = (int64_t)a.nfb * chunks;
     for (int S = 1; S <= most && (S == 1 || S * 2 <= KB); S *= 2) {
-      if (S > 1 && tiles > gemm16_clusters<false, kGated, kMats, kNT, kF16>(S, d.dev)) break;
+      if (S > 1 && tiles > gemm16_clusters<false, kGated, kMats, kNT, kF16, kSeg>(S, d.dev)) break;
       const float kb = (float)((KB + S - 1) / S);
       const float load = kb * (128 * kMats + nt) * (128.f / 94e3f), mma = kb * kMats * (nt > 128 ? 0.26f : 0.16f);
       const int64_t waves = (tiles * S + d.sms - 1) / d.sms;
@@ -61,10 +60,11 @@ static void gemm16_plan(Gemm16Args &a, const DeviceInfo &d) {
   }
 }
 
-template <bool kGated, bool kF16>
+template <bool kGated, bool kF16, bool kF32Out>
 static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const void *w, int64_t ldw, cudaStream_t s) {
   // gated: gate and up of 128 features and 128 rows a tile; else 128 outputs and 256 rows
-  constexpr int kMats = kGated ? 2 : 1, kNT = kGated ? 128 : 256;
+  // (fp32 outputs are summed in segments that the epilogue holds: half the rows)
+  constexpr int kMats = kGated ? 2 : 1, kNT = (kGated ? 128 : 256) / (kF32Out ? 2 : 1);
   DeviceInfo d;
   if (!device_info(&d)) return MOE_ERR_CUDA;
   CUtensorMap wm, x64, x16;
@@ -78,7 +78,7 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
   // outputs of a row, one vector, where the other way round it has one output
   // of 16 rows.  (8192 x 8192 x 2048 with bias, GELU and residual: see above.)
   const int64_t large = (int64_t)((a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256)) * ((a.rows + 127) / 128);
-  if (large >= d.sms) {
+  if (!kF32Out && large >= d.sms) {
     a.mat_off = kGated ? a.N : 128;
     a.nfb = (a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256);
     a.nt = 128;
@@ -89,10 +89,10 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
   a.mat_off = a.N;
   a.nfb = (a.N + 127) / 128;
   a.flip = 128;
-  gemm16_plan<kGated, kF16>(a, d);
+  gemm16_plan<kGated, kMats, kNT, kF16, kF32Out>(a, d);
   const int64_t tiles = (int64_t)a.nfb * ((a.rows + a.nt - 1) / a.nt);
   const int grid = a.splits > 1 ? (int)tiles * a.splits : (int)(tiles < d.sms ? tiles : d.sms);
-  return gemm16_launch<false, kGated, kMats, kNT, kF16>(a, grid, wm, x64, x16, d.dev, s);
+  return gemm16_launch<false, kGated, kMats, kNT, kF16, kF32Out>(a, grid, wm, x64, x16, d.dev, s);
 }
 
 }  // namespace moe
@@ -137,6 +137,10 @@ extern "C" MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void 
     if (f16) return gated ? linear_stream<true, true>(a, x, ldx, w, ldw, s) : linear_stream<false, true>(a, x, ldx, w, ldw, s);
     return gated ? linear_stream<true, false>(a, x, ldx, w, ldw, s) : linear_stream<false, false>(a, x, ldx, w, ldw, s);
   }
-  if (f16) return gated ? linear_gemm<true, true>(a, x, ldx, w, ldw, s) : linear_gemm<false, true>(a, x, ldx, w, ldw, s);
-  return gated ? linear_gemm<true, false>(a, x, ldx, w, ldw, s) : linear_gemm<false, false>(a, x, ldx, w, ldw, s);
+  if (a.y_f32) {
+    if (f16) return gated ? linear_gemm<true, true, true>(a, x, ldx, w, ldw, s) : linear_gemm<false, true, true>(a, x, ldx, w, ldw, s);
+    return gated ? linear_gemm<true, false, true>(a, x, ldx, w, ldw, s) : linear_gemm<false, false, true>(a, x, ldx, w, ldw, s);
+  }
+  if (f16) return gated ? linear_gemm<true, true, false>(a, x, ldx, w, ldw, s) : linear_gemm<false, true, false>(a, x, ldx, w, ldw, s);
+  return gated ? linear_gemm<true, false, false>(a, x, ldx, w, ldw, s) : linear_gemm<false, false, false>(a, x, ldx, w, ldw, s);
 }

@@ -306,3 +306,10 @@ assert (y[:4].float() - want).abs().max() < 0.01, y
 assert moe.moe_device_error() == 0
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
+
+
+@pytest.mark.parametrize("T,N,K,gated", [(20, 130, 4096, False), (333, 1500, 2048, False), (1000, 2050, 4096, False),
+                                         (300, 700, 4096, True), (40, 128, 16384, False)])
+def test_long_sums_keep_fp32_accuracy(T, N, K, gated):
+    """fp32 outputs of long sums: 2^-20 of the values as a whole (check_random's bound), whatever K."""
+    check_random(T, N, K, "bf16", "none", gated, True, False, True, 0, T + K)
