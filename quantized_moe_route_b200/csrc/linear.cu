@@ -18,11 +18,14 @@ static moe_status linear_stream(const Gemm16Args &g, const void *x, int64_t ldx,
   a.g = g;
   a.R = kGated ? 2 * per : per;
   a.strips = (g.N + per - 1) / per;
-  a.group_log2 = g.K > 512 ? 4 : g.K > 256 ? 3 : 2;  // 64 inputs a warp at least
+  a.group_log2 = g.K > 512 ? 3 : g.K > 256 ? 2 : 1;  // a pair of 64-input columns a warp at least
+  a.whole = g.K % 64 == 0;
   CUtensorMap wm, xm;
   const bool two = g.rows > 8;
-  if (!gemm16_map(&wm, w, (int64_t)g.N * (kGated ? 2 : 1), g.K, ldw, per, kF16) ||
-      !gemm16_map(&xm, x, g.rows, g.K, ldx, two ? 16 : 8, kF16)) {
+  const int64_t wrows = (int64_t)g.N * (kGated ? 2 : 1);
+  const int xrows = two ? 16 : 8;
+  if (!(a.whole ? gemm16_map3(&wm, w, wrows, g.K, ldw, per, kLsCols, kF16) && gemm16_map3(&xm, x, g.rows, g.K, ldx, xrows, kLsCols, kF16)
+                : gemm16_map(&wm, w, wrows, g.K, ldw, per, kF16) && gemm16_map(&xm, x, g.rows, g.K, ldx, xrows, kF16))) {
     set_cuda_error(cudaErrorInvalidValue);
     return MOE_ERR_CUDA;
   }
