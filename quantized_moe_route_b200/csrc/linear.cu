@@ -1,16 +1,21 @@
-// linear.cu -- y = act(x w^T + bias) + residual on 16-bit weights: up to 16
-// rows of x as a weight stream, more on the 5th-generation tensor cores.
+// linear.cu -- y = act(x w^T + bias) + residual on 16-bit weights: few rows of
+// x as a weight stream, more on the 5th-generation tensor cores.
 #include "gemm16.cuh"
 #include "linear_stream.cuh"
 
 namespace moe {
 
-constexpr int kLinearStreamRows = 16;
+// Rows of x up to which a linear is a weight stream: 16; and 32 where each SM
+// has one strip of outputs and K >= 512, so that x is loaded once (2048 x 2048,
+// 32 rows: 5.3 us against 6.6 on the tensor-core tiles, 2048 x 8192 10.3 / 13.6;
+// 8192 x 2048 15.1 / 10.5, 1000 x 100 5.8 / 3.9).
+inline bool linear_streams(int T, int N, int K, bool gated, int sms) {
+  return T <= 16 || (T <= 32 && K >= 512 && N <= (gated ? 8 : 16) * sms);
+}
 
 template <bool kGated, bool kF16>
-static moe_status linear_stream(const Gemm16Args &g, const void *x, int64_t ldx, const void *w, int64_t ldw, cudaStream_t s) {
-  DeviceInfo d;
-  if (!device_info(&d)) return MOE_ERR_CUDA;
+static moe_status linear_stream(const Gemm16Args &g, const void *x, int64_t ldx, const void *w, int64_t ldw,
+                                const DeviceInfo &d, cudaStream_t s) {
   // equal strips: as few to an SM as 16 rows each allow, of as few rows as that takes
   const int most = kGated ? 8 : 16;
   const int per_sm = (g.N + most * d.sms - 1) / (most * d.sms), per = (g.N + per_sm * d.sms - 1) / (per_sm * d.sms);
@@ -21,17 +26,18 @@ static moe_status linear_stream(const Gemm16Args &g, const void *x, int64_t ldx,
   a.group_log2 = g.K > 512 ? 3 : g.K > 256 ? 2 : 1;  // a pair of 64-input columns a warp at least
   a.whole = g.K % 64 == 0;
   CUtensorMap wm, xm;
-  const bool two = g.rows > 8;
+  const int nb = g.rows > 16 ? 4 : g.rows > 8 ? 2 : 1;
   const int64_t wrows = (int64_t)g.N * (kGated ? 2 : 1);
-  const int xrows = two ? 16 : 8;
+  const int xrows = 8 * nb;
   if (!(a.whole ? gemm16_map3(&wm, w, wrows, g.K, ldw, per, kLsCols, kF16) && gemm16_map3(&xm, x, g.rows, g.K, ldx, xrows, kLsCols, kF16)
                 : gemm16_map(&wm, w, wrows, g.K, ldw, per, kF16) && gemm16_map(&xm, x, g.rows, g.K, ldx, xrows, kF16))) {
     set_cuda_error(cudaErrorInvalidValue);
     return MOE_ERR_CUDA;
   }
   const int grid = a.strips < d.sms ? a.strips : d.sms;
-  return two ? linear_stream_launch<kGated, kF16, 2>(a, grid, wm, xm, d.dev, s)
-             : linear_stream_launch<kGated, kF16, 1>(a, grid, wm, xm, d.dev, s);
+  return nb == 4   ? linear_stream_launch<kGated, kF16, 4>(a, grid, wm, xm, d.dev, s)
+         : nb == 2 ? linear_stream_launch<kGated, kF16, 2>(a, grid, wm, xm, d.dev, s)
+                   : linear_stream_launch<kGated, kF16, 1>(a, grid, wm, xm, d.dev, s);
 }
 
 // The rows of a tile and the CTAs that share its K: the least of a model of
@@ -64,12 +70,11 @@ static void gemm16_plan(Gemm16Args &a, const DeviceInfo &d) {
 }
 
 template <bool kGated, bool kF16, bool kF32Out>
-static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const void *w, int64_t ldw, cudaStream_t s) {
+static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const void *w, int64_t ldw, const DeviceInfo &d,
+                              cudaStream_t s) {
   // gated: gate and up of 128 features and 128 rows a tile; else 128 outputs and 256 rows
   // (fp32 outputs are summed in segments that the epilogue holds: half the rows)
   constexpr int kMats = kGated ? 2 : 1, kNT = (kGated ? 128 : 256) / (kF32Out ? 2 : 1);
-  DeviceInfo d;
-  if (!device_info(&d)) return MOE_ERR_CUDA;
   CUtensorMap wm, x64, x16;
   if (!gemm16_map(&wm, w, (int64_t)a.N * (kGated ? 2 : 1), a.K, ldw, 128, kF16) ||
       !gemm16_map(&x64, x, a.rows, a.K, ldx, 64, kF16) || !gemm16_map(&x16, x, a.rows, a.K, ldx, 16, kF16)) {
@@ -135,15 +140,14 @@ extern "C" MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void 
   a.err = device_error_word();
   if (!a.err) return MOE_ERR_CUDA;
   cudaStream_t s = as_stream(stream);
-  const bool f16 = dtype == MOE_F16;
-  if (T <= kLinearStreamRows) {
-    if (f16) return gated ? linear_stream<true, true>(a, x, ldx, w, ldw, s) : linear_stream<false, true>(a, x, ldx, w, ldw, s);
-    return gated ? linear_stream<true, false>(a, x, ldx, w, ldw, s) : linear_stream<false, false>(a, x, ldx, w, ldw, s);
-  }
-  if (a.y_f32) {
-    if (f16) return gated ? linear_gemm<true, true, true>(a, x, ldx, w, ldw, s) : linear_gemm<false, true, true>(a, x, ldx, w, ldw, s);
-    return gated ? linear_gemm<true, false, true>(a, x, ldx, w, ldw, s) : linear_gemm<false, false, true>(a, x, ldx, w, ldw, s);
-  }
-  if (f16) return gated ? linear_gemm<true, true, false>(a, x, ldx, w, ldw, s) : linear_gemm<false, true, false>(a, x, ldx, w, ldw, s);
-  return gated ? linear_gemm<true, false, false>(a, x, ldx, w, ldw, s) : linear_gemm<false, false, false>(a, x, ldx, w, ldw, s);
+  DeviceInfo d;
+  if (!device_info(&d)) return MOE_ERR_CUDA;
+  const bool f16 = dtype == MOE_F16, stream_w = linear_streams(T, N, K, gated, d.sms);
+#define MOE_LINEAR(GATED, F16)                                                        \
+  (stream_w    ? linear_stream<GATED, F16>(a, x, ldx, w, ldw, d, s)                   \
+   : a.y_f32   ? linear_gemm<GATED, F16, true>(a, x, ldx, w, ldw, d, s)               \
+               : linear_gemm<GATED, F16, false>(a, x, ldx, w, ldw, d, s))
+  if (f16) return gated ? MOE_LINEAR(true, true) : MOE_LINEAR(false, true);
+  return gated ? MOE_LINEAR(true, false) : MOE_LINEAR(false, false);
+#undef MOE_LINEAR
 }

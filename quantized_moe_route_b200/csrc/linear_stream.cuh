@@ -1,4 +1,4 @@
-// linear_stream.cuh -- the linear for up to 16 rows of x: a weight stream.
+// linear_stream.cuh -- the linear for up to 32 rows of x: a weight stream.
 //
 // With few rows the product is as fast as its weights arrive.  A CTA takes
 // strips of R outputs (R <= 16, chosen so that the strips divide evenly over
@@ -33,7 +33,7 @@ struct LinearStreamArgs {
 
 template <int NB>
 struct LinearStreamCfg {
-  static constexpr int kStages = NB == 1 ? 4 : 3;                     // per warp: 96 to 128 KB of weights in flight
+  static constexpr int kStages = NB == 1 ? 4 : NB == 2 ? 3 : 2;                     // per warp: 96 to 128 KB of weights in flight
   static constexpr uint32_t kXOff = kLsCols * 2048;                   // 16 weight rows, then 8 NB rows of x
   static constexpr uint32_t kStage = kXOff + kLsCols * NB * 1024;
   static constexpr uint32_t kPartOff = kLsWarps * kStages * kStage;
