@@ -644,7 +644,8 @@ MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer, const uint
  * (moe_route_shared, moe_permute).  Entries of offsets outside [0, rows] are
  * clamped; rows that no expert owns are left as they were.
  * Workspace: moe_prefill_bf16_workspace_bytes(rows, F) bytes, 16-byte
- * aligned; after the call its first rows * F * 2 bytes hold h (bf16 [rows][F]).
+ * aligned, its contents unimportant; after the call its first rows * F * 2
+ * bytes hold h (bf16 [rows][F]).  Calls that share it must not overlap in time.
  * Requirements: H % 64 == 0, F % 64 == 0, E <= 1024, offsets non-decreasing
  * with offsets[0] == 0 and offsets[E] == rows; pointers 16-byte aligned.
  * rows == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, WORKSPACE, CUDA.

@@ -40,7 +40,6 @@
 #include "decode_common.cuh"
 #include "decode_items.cuh"
 #include "route.cuh"
-#include "tcgen05.cuh"
 #include "w16.cuh"
 
 namespace moe {

@@ -28,7 +28,6 @@
 // memory, and every CTA adds up its share of the rows in rank order through
 // distributed shared memory (a fixed order: the same bits every call).
 #pragma once
-#include "tcgen05.cuh"
 #include "w16.cuh"
 
 namespace moe {

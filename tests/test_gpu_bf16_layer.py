@@ -292,7 +292,7 @@ def check_grouped(seed, counts, H, F, extra=0):
     assert moe.moe_device_error() == 0
     assert (y[rows:] == 7.0).all(), "rows of no expert were written"
     assert (ws[n:] == 0x5A).all()
-    h = ws[:n].view(BF).view(rows + extra, F)[:rows]
+    h = ws[:(rows + extra) * F * 2].view(BF).view(rows + extra, F)[:rows]
     at = 0
     for e, c in enumerate(counts):
         if c:
@@ -333,6 +333,35 @@ def test_grouped_offsets_past_the_rows_are_clamped():
     for e, (a, b) in enumerate([(0, 30), (30, 60), (60, 100)]):
         want, tol = layer.rows(e, x[a:b])[0][:2]
         check_close(y[a:b], want, tol + 2.0 ** -8 * (want.abs() + tol), f"expert {e}")
+
+
+def test_grouped_captured_with_many_tiles():
+    """Enough tiles for the counters (cleared in the graph): replays on new groups, and twice on the same."""
+    E, H, F, rows = 160, 64, 256, 3000
+    layer = Layer16(115, E, H, F, sigma=0.1)
+    gen = torch.Generator(device="cuda").manual_seed(116)
+    x, y = normal(gen, (rows, H), 1.0), torch.empty((rows, H), dtype=BF, device="cuda")
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_prefill_bf16_workspace_bytes(rows, F), dtype=torch.uint8, device="cuda").fill_(0xFF)
+    call = lambda: moe.moe_ffn_grouped_prefill_bf16(layer.desc, x, offsets, y, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    rng = np.random.RandomState(117)
+    for i in range(3):
+        p = rng.gamma(0.3, size=E) + 1e-9
+        off = np.concatenate([[0], np.cumsum(rng.multinomial(rows, p / p.sum()))])
+        offsets.copy_(torch.tensor(off, dtype=torch.int32))
+        for _ in range(2):
+            y.fill_(7.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert moe.moe_device_error() == 0
+            for e in np.flatnonzero(np.diff(off)):
+                a, b = off[e], off[e + 1]
+                want, tol = layer.rows(int(e), x[a:b])[0][:2]
+                assert ((y[a:b].double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all(), (i, e)
 
 
 def test_grouped_captured_follows_new_offsets():
