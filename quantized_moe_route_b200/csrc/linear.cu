@@ -1,6 +1,7 @@
 // linear.cu -- y = act(x w^T + bias) + residual on 16-bit weights: few rows of
 // x as a weight stream, more on the 5th-generation tensor cores.
 #include "gemm16.cuh"
+#include "gemm16_pair.cuh"
 #include "linear_stream.cuh"
 
 namespace moe {
@@ -81,18 +82,27 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
     set_cuda_error(cudaErrorInvalidValue);
     return MOE_ERR_CUDA;
   }
-  // Enough tiles of 128 rows and two weight blocks (256 outputs, or gate and up
-  // of 128) for every SM: the rows go on M, and a lane of the epilogue holds 16
-  // outputs of a row, one vector, where the other way round it has one output
-  // of 16 rows.  (8192 x 8192 x 2048 with bias, GELU and residual: see above.)
-  const int64_t large = (int64_t)((a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256)) * ((a.rows + 127) / 128);
-  if (!kF32Out && large >= d.sms) {
+  // Tiles of 128 rows and two weight blocks (256 outputs, or gate and up of 128)
+  // for most SMs: the rows go on M, and a lane of the epilogue holds 16 outputs
+  // of a row, one vector, where the other way round it has one output of 16
+  // rows.  (2048 x 2048, 2048 rows = 128 tiles: 16.6 us against 21.5; 1280 rows =
+  // 80 tiles: 16.6 / 15.7; gated, 640 rows = 80 tiles: 16.7 / 17.8.)
+  const int nfb = (a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256);
+  const int64_t tiles1 = (int64_t)nfb * ((a.rows + 127) / 128), tiles2 = (int64_t)nfb * ((a.rows + 255) / 256);
+  if (!kF32Out && tiles1 >= (kGated ? d.sms / 2 : 3 * d.sms / 4)) {
     a.mat_off = kGated ? a.N : 128;
-    a.nfb = (a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256);
+    a.nfb = nfb;
     a.nt = 128;
     a.splits = 1;
     a.flip = 0;
-    return gemm16_launch<false, kGated, 2, 128, kF16>(a, d.sms, wm, x64, x16, d.dev, s);
+    // Pairs of SMs where there is a tile for every pair, no more rounds of them,
+    // and K is long enough to pay for the pairing: 8192 rows of 2048 x 8192 with
+    // bias, GELU and residual 248 us against 270 one after another (plain 207 /
+    // 240); 2048 x 512, 4096 rows 14.7 / 14.1.
+    const int pairs = d.sms / 2;
+    if (a.K >= 1024 && tiles2 >= pairs && (tiles2 + pairs - 1) / pairs <= (tiles1 + d.sms - 1) / d.sms)
+      return gemm16_pair_launch<kGated, kF16>(a, pairs, wm, x64, x16, d.dev, s);
+    return gemm16_launch<false, kGated, 2, 128, kF16>(a, (int)(tiles1 < d.sms ? tiles1 : d.sms), wm, x64, x16, d.dev, s);
   }
   a.mat_off = a.N;
   a.nfb = (a.N + 127) / 128;

@@ -313,3 +313,57 @@ assert moe.moe_device_error() == 0
 def test_long_sums_keep_fp32_accuracy(T, N, K, gated):
     """fp32 outputs of long sums: 2^-20 of the values as a whole (check_random's bound), whatever K."""
     check_random(T, N, K, "bf16", "none", gated, True, False, True, 0, T + K)
+
+
+# tiles for all SMs: rows on M (alone, K < 1024; on pairs of SMs, K >= 1024), ragged in rows, outputs and K
+@pytest.mark.parametrize("T,N,K,dtype,gated,pad", [
+    (2432, 2048, 64, "bf16", False, 0), (1921, 2049, 136, "f16", False, 0), (9000, 300, 520, "f16", True, 3),
+    (20000, 250, 72, "bf16", False, 0), (2500, 2048, 1024, "bf16", False, 0), (2433, 2047, 1096, "f16", False, 5),
+    (2700, 1300, 1032, "bf16", True, 0), (129 * 128, 130, 1025, "bf16", False, 1), (4225, 1200, 2048, "f16", False, 8)])
+def test_large_products_are_exact_on_integers(T, N, K, dtype, gated, pad):
+    gen = torch.Generator(device="cuda").manual_seed(T + N + K)
+    dt, rows = DT[dtype], 2 * N if gated else N
+    _, x = padded(T, K, up8(K) + 8 * (T % 2), dt)
+    _, w = padded(rows, K, up8(K), dt)
+    x.copy_(ints(gen, (T, K), dt, 1))
+    w.copy_(ints(gen, (rows, K), dt, 1))
+    bias = ints(gen, (rows,), dt, 2)
+    rbuf, r = padded(T, N, N + pad, dt, 5.0)
+    r.copy_(ints(gen, (T, N), dt, 9))
+    v = x.double() @ w.double().t() + bias.double()
+    want = (v[:, :N].clamp(min=0) * v[:, N:] if gated else v.clamp(min=0)) + r.double()
+    moe.moe_linear(x, w, r, bias=bias, residual=r, act=moe.MOE_ACT_RELU, gated=gated)  # in place
+    assert torch.equal(r, want.float().to(dt))
+    assert (rbuf[:, N:] == 5.0).all()
+    assert moe.moe_device_error() == 0
+
+
+@pytest.mark.parametrize("act,gated", [("gelu_tanh", False), ("silu", True), ("gelu", True)])
+def test_large_products_random(act, gated):
+    check_random(2600, 1100, 1200, "bf16", act, gated, True, True, False, 8, 5)
+    check_random(4200, 1111, 200, "f16", act, gated, True, True, False, 8, 6)
+
+
+def test_large_products_same_bits_and_captured():
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    x, w = torch.randn((2560, 1024), generator=gen, device="cuda").bfloat16(), torch.randn((2048, 1024), generator=gen, device="cuda").bfloat16()
+    ys = [torch.empty((2560, 2048), device="cuda").bfloat16() for _ in range(3)]
+    moe.moe_linear(x, w, ys[0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):  # two at once
+        for s, y in zip(streams, ys[1:]):
+            moe.moe_linear(x, w, y, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], ys[1]) and torch.equal(ys[0], ys[2])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_linear(x, w, ys[1])
+        moe.moe_linear(x, w, ys[2], residual=ys[1])
+    x.copy_(torch.randn((2560, 1024), generator=gen, device="cuda"))
+    g.replay()
+    torch.cuda.synchronize()
+    moe.moe_linear(x, w, ys[0])
+    assert torch.equal(ys[0], ys[1])
+    moe.moe_linear(x, w, ys[0], residual=ys[0])
+    assert torch.equal(ys[0], ys[2]) and moe.moe_device_error() == 0
