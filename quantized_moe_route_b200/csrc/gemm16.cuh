@@ -33,7 +33,8 @@
 namespace moe {
 
 constexpr int kG16BK = 64;
-constexpr int kG16Stages = 4;
+constexpr uint32_t kG16Ring = 4 * 48 * 1024;  // bytes of the stage ring: 4 stages of the largest tiles, more of smaller ones
+constexpr int kG16MaxStages = 12;
 constexpr int kG16Seg = 8;          // k blocks that one accumulation runs over where y is fp32
 constexpr int kG16EpiWarps = 12;  // three to a lane quarter of tensor memory
 constexpr int kG16Threads = (2 + kG16EpiWarps) * 32;
@@ -47,6 +48,7 @@ struct Gemm16Args {
   int mat_off;             // weight rows from a tile's block 0 to its block 1
   int nfb;                 // output blocks per row chunk
   int nt;                  // rows per chunk (at most kNT, a multiple of 16)
+  int stages;              // of the ring (set by the launch)
   int flip;                // tiles of more rows are issued with the rows on M (two blocks of up to 128 rows)
   int splits;              // CTAs of a cluster that share a tile (1: none, persistent over tiles)
   const uint16_t *bias, *residual;
@@ -60,8 +62,8 @@ template <int kMats, int kNT>
 struct Gemm16Cfg {
   static constexpr uint32_t kABytes = kMats * 128 * 128;  // 128 rows of 64 channels per block
   static constexpr uint32_t kBBytes = kNT * 128;
-  static constexpr uint32_t kStage = kABytes + kBBytes;
-  static constexpr uint32_t kTailOff = kG16Stages * kStage;
+  static constexpr uint32_t kTailOff = kG16Ring;
+  static_assert(4 * (kABytes + kBBytes) <= kG16Ring, "four stages");
   static constexpr uint32_t kTableInts = 1024 + 1;
   static constexpr uint32_t kSmemBytes = kTailOff + 1024 /* alignment */ + 256 + kTableInts * 4;
   static constexpr uint32_t kAccCols = kMats * kNT;
@@ -368,16 +370,19 @@ __global__ void __launch_bounds__(kG16Threads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (keeps the address space known)
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kTailOff);
-  uint64_t *empty = full + kG16Stages;
-  uint64_t *acc_full = empty + kG16Stages;  // [2]
+  uint64_t *empty = full + kG16MaxStages;
+  uint64_t *acc_full = empty + kG16MaxStages;  // [2]
   uint64_t *acc_empty = acc_full + 2;       // [2]
   uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(acc_empty + 2);
   volatile int *abort_s = reinterpret_cast<volatile int *>(tmem_base_s + 1);
   int *start = reinterpret_cast<int *>(smem + C::kTailOff + 256);  // [E + 1]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // a stage holds the weights and the nt rows that a chunk has at most
+  const uint32_t stage = C::kABytes + (uint32_t)a.nt * 128u;
+  const int nst = a.stages;
   if (tid == 0) {
-    for (int s = 0; s < kG16Stages; ++s) {
+    for (int s = 0; s < nst; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -430,17 +435,17 @@ __global__ void __launch_bounds__(kG16Threads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t it = 0;
+      int s = 0;
+      uint32_t ph = 0;
       for (int t = t0; t < ntiles && !*abort_s; t += G) {
         const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
         const int nrows = (ti.nvalid + 15) & ~15;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % kG16Stages;
-          if (!mbar_wait_sleep(&empty[s], ((it / kG16Stages) & 1u) ^ 1u, kG16WaitPolls)) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_sleep(&empty[s], ph ^ 1u, kG16WaitPolls)) {
             fail();
             break;
           }
-          uint8_t *at = smem + s * C::kStage, *bt = at + C::kABytes;
+          uint8_t *at = smem + s * stage, *bt = at + C::kABytes;
           mbar_arrive_expect_tx(&full[s], C::kABytes + (uint32_t)nrows * 128u);
 #pragma unroll
           for (int m = 0; m < kMats; ++m)
@@ -448,17 +453,23 @@ __global__ void __launch_bounds__(kG16Threads, 1)
           int r = 0;  // boxes of 64 rows, then of 16
           for (; r + 64 <= nrows; r += 64) tma_load_2d(bt + r * 128, &x64_map, kb * kG16BK, ti.row0 + r, &full[s]);
           for (; r < nrows; r += 16) tma_load_2d(bt + r * 128, &x16_map, kb * kG16BK, ti.row0 + r, &full[s]);
+          if (++s == nst) s = 0, ph ^= 1u;
         }
       }
-      // the last load issued into each stage lands before the CTA leaves
+      // the last load issued into each stage lands before the CTA leaves: from
+      // stage s on in the order of issue (a stage not used yet: its barrier's
+      // phase before the first counts as complete)
       if (*abort_s)
-        for (uint32_t j = it > kG16Stages ? it - kG16Stages : 0u; j < it; ++j)
-          mbar_wait_sleep(&full[j % kG16Stages], (j / kG16Stages) & 1u, kG16WaitPolls);
+        for (int i = 0; i < nst; ++i) {
+          mbar_wait_sleep(&full[s], ph ^ 1u, kG16WaitPolls);
+          if (++s == nst) s = 0, ph ^= 1u;
+        }
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
-      uint32_t it = 0, tc = 0;
+      int s = 0;
+      uint32_t ph = 0, tc = 0;
       for (int t = t0; t < ntiles && !*abort_s; t += G) {
         const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
         const uint32_t idesc = idesc_16_f32(kCanFlip && ti.nvalid > a.flip ? 256 : (ti.nvalid + 15) & ~15, kF16);
@@ -472,15 +483,14 @@ __global__ void __launch_bounds__(kG16Threads, 1)
           }
           tc_fence_after();
           const int first = kb, last = kSeg ? min(kb1, kb + kG16Seg) : kb1;
-          for (; kb < last; ++kb, ++it) {
-            const int s = it % kG16Stages;
-            if (!mbar_wait_sleep(&full[s], (it / kG16Stages) & 1u, kG16WaitPolls)) {
+          for (; kb < last; ++kb) {
+            if (!mbar_wait_sleep(&full[s], ph, kG16WaitPolls)) {
               fail();
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t ad = desc0 + ((uint32_t)s * C::kStage >> 4), bd = ad + (C::kABytes >> 4);
+            const uint64_t ad = desc0 + ((uint32_t)s * stage >> 4), bd = ad + (C::kABytes >> 4);
             if (kCanFlip && ti.nvalid > a.flip) {
 #pragma unroll
               for (int kk = 0; kk < kG16BK / 16; ++kk)
@@ -494,6 +504,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
                               (kb > first || kk) ? 1u : 0u);
             }
             tc_commit(&empty[s]);
+            if (++s == nst) s = 0, ph ^= 1u;
           }
           if (ok) tc_commit(&acc_full[tc & 1u]);
         }
@@ -740,7 +751,7 @@ int gemm16_clusters(int splits, int dev) {
 }
 
 template <bool kGrouped, bool kGated, int kMats, int kNT, bool kF16, bool kSeg = false>
-moe_status gemm16_launch(const Gemm16Args &a, int grid, const CUtensorMap &w, const CUtensorMap &x64,
+moe_status gemm16_launch(Gemm16Args a, int grid, const CUtensorMap &w, const CUtensorMap &x64,
                          const CUtensorMap &x16, int dev, cudaStream_t stream) {
   using C = Gemm16Cfg<kMats, kNT>;
   auto kern = gemm16_kernel<kGrouped, kGated, kMats, kNT, kF16, kSeg>;
@@ -753,6 +764,8 @@ moe_status gemm16_launch(const Gemm16Args &a, int grid, const CUtensorMap &w, co
     }
     attr_done[dev].store(true, std::memory_order_release);
   }
+  const int fit = (int)(kG16Ring / (C::kABytes + (uint32_t)a.nt * 128u));
+  a.stages = fit < kG16MaxStages ? fit : kG16MaxStages;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kG16Threads);
