@@ -682,6 +682,11 @@ MOE_API moe_status moe_device_error(int *out, moe_stream_t stream);
  *     whose weight producer issues no loads, every pipeline wait bounded by
  *     `polls` sleeping polls (each at most ~10 us).  Raises
  *     MOE_DEVERR_PREFILL_WAIT; the workspace (h) is left unspecified.
+ *   - moe_debug_starve_decode_bf16: moe_decode_layer_bf16 (logits given, no
+ *     shared expert) whose gate/up units consume their weights but publish no
+ *     h, with the wait for h bounded by `polls` polls.  Raises
+ *     MOE_DEVERR_DECODE_H_WAIT; y is left unspecified, zero-fill the workspace
+ *     before its next use.
  * Arguments and errors as for the calls they derive from; polls >= 1.
  */
 MOE_API moe_status moe_debug_starve_decode(const moe_w4_layer *layer, const uint16_t *x,
@@ -692,6 +697,10 @@ MOE_API moe_status moe_debug_starve_prefill(const moe_w4_layer *layer, const uin
                                             const int32_t *offsets, int rows, void *ws,
                                             size_t ws_bytes, unsigned int polls,
                                             moe_stream_t stream);
+
+MOE_API moe_status moe_debug_starve_decode_bf16(const moe_bf16_layer *layer, const uint16_t *x,
+                                                float *logits, int T, int k, uint16_t *y, void *ws,
+                                                size_t ws_bytes, unsigned int polls, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

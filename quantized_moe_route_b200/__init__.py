@@ -110,6 +110,8 @@ SIGNATURES = {
                                    _vp, _sz, _vp]),
     "moe_prefill_bf16_workspace_bytes": (_sz, [_i, _i]),
     "moe_ffn_grouped_prefill_bf16": (_i, [ctypes.POINTER(moe_bf16_layer), _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "moe_debug_starve_decode_bf16": (_i, [ctypes.POINTER(moe_bf16_layer), _vp, _vp, _i, _i, _vp, _vp, _sz, ctypes.c_uint,
+                                          _vp]),
     "moe_device_error": (_i, [ctypes.POINTER(ctypes.c_int), _vp]),
     "moe_debug_starve_decode": (_i, [ctypes.POINTER(moe_w4_layer), _vp, _vp, _i, _i, _vp, _vp, _sz, ctypes.c_uint,
                                      _vp]),
@@ -512,3 +514,9 @@ def moe_debug_starve_prefill(layer: moe_w4_layer, x_perm, offsets, ws, polls, st
     _check(lib().moe_debug_starve_prefill(ctypes.byref(layer), _p(x_perm), _p(offsets), rows, _p(ws),
                                           ws.numel() * ws.element_size(), polls, _stream(stream)),
            "moe_debug_starve_prefill")
+
+
+def moe_debug_starve_decode_bf16(layer: moe_bf16_layer, x, logits, k, y, ws, polls, stream=None):
+    _check(lib().moe_debug_starve_decode_bf16(ctypes.byref(layer), _p(x), _p(logits), x.shape[0], k, _p(y), _p(ws),
+                                              ws.numel() * ws.element_size(), polls, _stream(stream)),
+           "moe_debug_starve_decode_bf16")

@@ -68,6 +68,8 @@ struct DecodeBf16Args {
   float *w;
   int *err;
   int T, kk, shared, E, H, F;  // kk: rows per token (k + shared)
+  uint32_t h_polls;            // bound of phase B's wait for h (polls of about 1 us)
+  int starve;                  // test hook: phase A publishes no h
   int nst_log2;                // ring stages
   int R;                       // output channels of a phase B strip (at most 16)
   uint32_t hb_bytes;           // per-warp h buffer
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int n = nb * 8 + 2 * t4 + i;
-          if (n < ntok) {
+          if (n < ntok && !a.starve) {
             const int t = nth_bit(mask, n);
             const float h = activate(v[i], MOE_ACT_SILU) * v[2 + i];
             const float hi = bf16_bits_to_f32(f32_to_bf16_bits(h));
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
                 const int row = __shfl_sync(0xffffffffu, my_row, n0);
                 ld_relaxed_u64x2(a.hbuf + (size_t)row * F + c * kB16KC + k1 + lane * 2, wv[0][0], wv[0][1]);
                 if (__all_sync(0xffffffffu, (unsigned int)wv[0][0] == epoch && (unsigned int)wv[0][1] == epoch)) break;
-                if (++spins > kB16Polls || __any_sync(0xffffffffu, misc[0])) break;  // (the loop below ends the wait)
+                if (++spins > a.h_polls || __any_sync(0xffffffffu, misc[0])) break;  // (the loop below ends the wait)
                 __nanosleep(100);
               }
               while (true) {  // all of the words, again until all are this call's
@@ -552,8 +554,8 @@ __global__ void __launch_bounds__(kB16Threads, 1)
                       ((unsigned int)wv[i][0] != epoch || (unsigned int)wv[i][1] != epoch))
                     mine = false;
                 if (__all_sync(0xffffffffu, mine)) break;
-                if (++spins > kB16Polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
-                if (__any_sync(0xffffffffu, spins > kB16Polls || misc[0])) {
+                if (++spins > a.h_polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
+                if (__any_sync(0xffffffffu, spins > a.h_polls || misc[0])) {
                   ok = false;
                   break;
                 }
@@ -729,11 +731,11 @@ extern "C" MOE_API size_t moe_decode_layer_bf16_workspace_bytes(int T, int k, in
   return kB16CtrlBytes + sizeof(unsigned long long) * ((size_t)T * (k + shared) * F + (size_t)T * (E + 1));
 }
 
-extern "C" MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer, const uint16_t *x, const uint16_t *wr,
-                                                    float *logits, int T, int k, int shared,
-                                                    const uint16_t *shared_gate, const uint16_t *residual, uint16_t *y,
-                                                    int32_t *idx, float *w, void *ws, size_t ws_bytes,
-                                                    moe_stream_t stream) {
+// polls: bound of phase B's wait for h; starve: the test hook
+static moe_status decode_layer_bf16(const moe_bf16_layer *layer, const uint16_t *x, const uint16_t *wr, float *logits,
+                                    int T, int k, int shared, const uint16_t *shared_gate, const uint16_t *residual,
+                                    uint16_t *y, int32_t *idx, float *w, void *ws, size_t ws_bytes, unsigned int polls,
+                                    int starve, moe_stream_t stream) {
   if (!layer || T < 0 || k <= 0 || shared < 0 || shared > 1) return MOE_ERR_INVALID_ARG;
   const int E = layer->E, H = layer->H, F = layer->F, kk = k + shared, Er = E - shared;
   if (Er <= 0 || H <= 0 || F <= 0 || k > Er || (shared_gate && !shared)) return MOE_ERR_INVALID_ARG;
@@ -771,7 +773,26 @@ extern "C" MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer,
   a.E = E;
   a.H = H;
   a.F = F;
+  a.h_polls = polls;
+  a.starve = starve;
   cudaStream_t s = as_stream(stream);
   if (T <= kB16JobTok) return Er <= 256 ? decode_bf16_launch<8, 8>(a, s) : decode_bf16_launch<8, 32>(a, s);
   return Er <= 256 ? decode_bf16_launch<16, 8>(a, s) : decode_bf16_launch<16, 32>(a, s);
+}
+
+extern "C" MOE_API moe_status moe_decode_layer_bf16(const moe_bf16_layer *layer, const uint16_t *x, const uint16_t *wr,
+                                                    float *logits, int T, int k, int shared,
+                                                    const uint16_t *shared_gate, const uint16_t *residual, uint16_t *y,
+                                                    int32_t *idx, float *w, void *ws, size_t ws_bytes,
+                                                    moe_stream_t stream) {
+  return decode_layer_bf16(layer, x, wr, logits, T, k, shared, shared_gate, residual, y, idx, w, ws, ws_bytes, kB16Polls,
+                           0, stream);
+}
+
+extern "C" MOE_API moe_status moe_debug_starve_decode_bf16(const moe_bf16_layer *layer, const uint16_t *x, float *logits,
+                                                           int T, int k, uint16_t *y, void *ws, size_t ws_bytes,
+                                                           unsigned int polls, moe_stream_t stream) {
+  if (polls == 0) return MOE_ERR_INVALID_ARG;
+  return decode_layer_bf16(layer, x, nullptr, logits, T, k, 0, nullptr, nullptr, y, nullptr, nullptr, ws, ws_bytes, polls,
+                           1, stream);
 }

@@ -277,6 +277,26 @@ def test_decode_captured_replays_and_streams():
     assert moe.moe_device_error() == 0
 
 
+@pytest.mark.parametrize("T", [1, 3, 11])
+def test_decode_wait_that_runs_out_is_reported_and_leaves_the_gpu_usable(T):
+    """Phase A publishes no h: every wait of phase B gives up within its bound, the call ends, the error word names
+    the wait, and the next call on a cleared workspace is right."""
+    layer = Layer16(95, 16, 512, 256)
+    gen = torch.Generator(device="cuda").manual_seed(96)
+    x, lg = normal(gen, (T, 512), 1.0), torch.randn((T, 16), generator=gen, device="cuda")
+    ws, y = workspace(layer, T, 4, 0), torch.empty((T, 512), dtype=BF, device="cuda")
+    assert moe.moe_device_error() == 0
+    moe.moe_debug_starve_decode_bf16(layer.desc, x, lg, 4, y, ws, 500)
+    torch.cuda.synchronize()
+    assert moe.moe_device_error() == moe.MOE_DEVERR_DECODE_H_WAIT
+    assert moe.moe_device_error() == 0
+    ws.zero_()
+    y, _, _, _ = run_decode(layer, x, 4, lg=lg, ws=ws)
+    want, tol, _, _ = reference(layer, x, lg, 4, 0, None, None)
+    check_close(y, want, tol, "the call after")
+    assert moe.moe_device_error() == 0
+
+
 # ------------------------------------------------------------------ grouped
 def check_grouped(seed, counts, H, F, extra=0):
     E, rows = len(counts), sum(counts)
