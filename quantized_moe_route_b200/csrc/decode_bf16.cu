@@ -450,17 +450,20 @@ __global__ void __launch_bounds__(kB16Threads, 1)
           }
         } else {
           // rows 0-7 with tokens 0-3: columns b; rows 8-15 (the same weight rows)
-          // with tokens in 4-7: columns b + half.  An odd last column meets
-          // zeros (out of range, filled by the copy), with any x that exists.
+          // with tokens in 4-7: columns b + half.  An odd last column has no
+          // second: its weights are zeros (out of range, filled by the copy) and so
+          // is its x (any other may hold an infinity).
           const int half = (nch + 1) / 2;
 #pragma unroll 4
           for (int b = 0; b < half; ++b, wa += 1024, xo += 128) {
-            const uint8_t *xv = xa[0] + xo + (g >= 4 && b + half < nch ? half * 128 : 0);
+            const bool none = g >= 4 && b + half >= nch;
+            const uint8_t *xv = xa[0] + xo + (g >= 4 && !none ? half * 128 : 0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint4 w0 = ld16(wa + wo[i]), w1 = ld16(wa + half * 1024 + wo[i]);
               const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
-              const uint4 v = ld16(xv + 16 * i);
+              uint4 v = ld16(xv + 16 * i);
+              if (none) v = make_uint4(0, 0, 0, 0);
               mma_bf16_pure(acc[0][2 * i], f0r, v.x, v.y);
               mma_bf16_pure(acc[0][2 * i + 1], f1r, v.z, v.w);
             }
@@ -488,9 +491,12 @@ __global__ void __launch_bounds__(kB16Threads, 1)
           if (n < ntok && !a.starve) {
             const int t = nth_bit(mask, n);
             const float h = activate(v[i], MOE_ACT_SILU) * v[2 + i];
-            const float hi = bf16_bits_to_f32(f32_to_bf16_bits(h));
+            // h = hi + lo; an h that bf16 rounds to inf keeps its leading bits, an infinite one has lo = 0
+            float hi = bf16_bits_to_f32(f32_to_bf16_bits(h));
+            if (fabsf(hi) == INFINITY) hi = __uint_as_float(__float_as_uint(h) & 0xFFFF0000u);
+            const float lo = fabsf(hi) == INFINITY ? 0.f : h - hi;
             st_relaxed_u64(a.hbuf + (size_t)(t * kk + slot_j[slot * 16 + t]) * F + f0 + g,
-                           ((unsigned long long)cvt_bf16x2(hi, h - hi) << 32) | epoch);
+                           ((unsigned long long)cvt_bf16x2(hi, lo) << 32) | epoch);
           }
         }
       }

@@ -13,6 +13,8 @@ reference keeps h as it is.  Tolerance per element of a row output:
     relative), and bf16 rounding adds 2^-8 |y|.
 The relative L2 error is also held to rounding size: at most half a step, 2^-8.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -295,6 +297,45 @@ def test_decode_wait_that_runs_out_is_reported_and_leaves_the_gpu_usable(T):
     want, tol, _, _ = reference(layer, x, lg, 4, 0, None, None)
     check_close(y, want, tol, "the call after")
     assert moe.moe_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1, 4, 7])
+@pytest.mark.parametrize("H", [128, 192, 1088])
+def test_decode_infinite_input_gives_infinite_output(T, H):
+    """With weights above zero an infinite input makes every sum of its token +inf, wherever it lies, and no other
+    token's anything else (a product of an infinity with padding would make them NaN)."""
+    layer = Layer16(97, 8, H, 128)
+    layer.gu.abs_().add_(0.01)
+    layer.dn.abs_().add_(0.01)
+    gen = torch.Generator(device="cuda").manual_seed(98)
+    lg = torch.randn((T, 8), generator=gen, device="cuda")
+    for at in sorted({0, 63, 64, H - 65, H - 1}):
+        x = normal(gen, (T, H), 1.0).abs_()
+        x[T - 1, at] = float("inf")
+        y, _, _, _ = run_decode(layer, x, 2, lg=lg)
+        assert torch.isinf(y[T - 1]).all() and (y[T - 1] > 0).all(), at
+        assert torch.isfinite(y[: T - 1]).all(), at
+
+
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("ups, h", [((2.0**64, 0.0, 0.0), math.inf),
+                                    ((2.0**63, 2.0**63 * (1 - 2.0**-8), 2.0**53), 2.0**128 * (1 - 2.0**-9 + 2.0**-11))])
+def test_decode_h_at_the_end_of_the_range(T, ups, h):
+    """An h beyond fp32 is inf on its way to the down projection, and one that fp32 holds but that bf16 would round to
+    inf is finite.  One feature: silu(2^64) = 2^64, up the sum of three inputs' weights, down 2^-20."""
+    H, F = 128, 64
+    layer = Layer16(99, 4, H, F)
+    layer.gu.zero_()
+    layer.dn.zero_()
+    layer.gu[:, 0, 0] = 1.0
+    for i, u in enumerate(ups):
+        layer.gu[:, F, 1 + i] = u
+    layer.dn[:, :, 0] = 2.0**-20
+    x = torch.zeros((T, H), dtype=BF, device="cuda")
+    x[:, 0] = 2.0**64
+    x[:, 1:4] = 1.0
+    y, _, _, _ = run_decode(layer, x, 1, lg=torch.zeros((T, 4), device="cuda"))
+    assert torch.equal(y, torch.full_like(y, h * 2.0**-20))
 
 
 # ------------------------------------------------------------------ grouped
