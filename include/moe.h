@@ -614,8 +614,7 @@ typedef struct {
  * the residual itself; beyond that no output may overlap an input.
  * Each selected expert's weights are read once per call whatever the number
  * of tokens routed to it; sums are fp32 in a fixed order; h enters the down
- * projection with 16 significant bits or more (the int4 layer rounds it to
- * bf16's 8).  Source: the passages of moe_decode_layer_w4a16_router; the gate
+ * projection with 16 significant bits (the int4 layer rounds it to bf16's 8).  Source: the passages of moe_decode_layer_w4a16_router; the gate
  * on the shared expert is the Qwen3.5-MoE backbone's.
  * Workspace: moe_decode_layer_bf16_workspace_bytes(T, k, shared, E, H, F) (E =
  * layer->E) bytes, 16-byte aligned, zero-filled before its first use,

@@ -11,10 +11,13 @@
 // 7.1 TB/s over 148 CTAs with nothing else to do; the same bytes as 16 row
 // copies of 1 KB reach 2.8 TB/s, as four of 4 KB 4.5 TB/s.)
 //   phase A  unit = 4 or 8 features of one expert (their gate and up rows, all
-//            H inputs).  Units go round the CTAs; h is published as 8-byte
-//            words {h as a bf16 pair, call epoch} (single-copy atomic: a
-//            reader polls the words themselves, no fence or counter on the
-//            path).
+//            H inputs).  Units go round the CTAs; h is published as 16-byte
+//            words {four values of 24 bits, call epoch}, stored and loaded as one
+//            .b128 each (single-copy atomic: a reader polls the words
+//            themselves, no fence or counter on the path).  Every CTA of phase B
+//            reads all of h, so its bytes count: with 8-byte words {bf16 pair,
+//            epoch}, twice as many, 16 tokens take 128 us for 124, 4 tokens 45 / 42,
+//            one 20.1 / 19.9.
 //   phase B  a CTA owns R output channels (H / CTAs, at most 16) and runs
 //            every selected expert's rows of them, one warp per expert and four
 //            tokens (a busier expert's tile is loaded again, from L2): all k
@@ -54,13 +57,16 @@ constexpr int kB16JobTok = 4;                         // tokens of a phase B job
 constexpr int kB16MaxF = 1 << 20;
 constexpr int kB16MaxX = 166000;                      // bytes of x rows that fit beside two stages
 constexpr size_t kB16CtrlBytes = 4096;                // workspace head: epoch, done counter
+// The logit words lie between the head and h, at one place whatever the call's sizes: both kinds of words keep
+// their epoch where a call of other sizes would look for one.
+constexpr size_t kB16LogitBytes = 16 * 1025 * 8;
 constexpr uint32_t kB16Polls = 1u << 22;              // bound of a poll loop (of >= 32 ns sleeps)
 constexpr uint32_t kB16BarPolls = 1u << 19;           // bound of a barrier wait (polls suspend for some us)
 
 struct DecodeBf16Args {
   const uint16_t *gu, *dn, *x, *wr, *sg, *residual;
   float *logits;             // [T][Er]: the input, or with wr an optional output
-  unsigned long long *hbuf;  // [T kk][F] words {bf16 lo, bf16 hi, epoch}: h = hi + lo
+  ulonglong2 *hbuf;          // [T kk][F / 4] words {epoch, upper 16 bits of four values of h, their next 8 bits each}
   unsigned long long *lbuf;  // [T][Er + 1] words {fp32 logit, epoch}; entry Er: the shared expert's gate
   unsigned int *ctrl;        // [0] last epoch, [1] CTAs done
   uint16_t *y;
@@ -97,8 +103,21 @@ __device__ __forceinline__ void b16_consumer_sync() { asm volatile("bar.sync 1, 
 __device__ __forceinline__ void st_relaxed_u64(unsigned long long *p, unsigned long long v) {
   asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
-__device__ __forceinline__ void ld_relaxed_u64x2(const unsigned long long *p, unsigned long long &a, unsigned long long &b) {
-  asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "l"(p) : "memory");
+__device__ __forceinline__ void st_relaxed_b128(ulonglong2 *p, unsigned long long a, unsigned long long b) {
+  asm volatile("{\n\t.reg .b128 t;\n\tmov.b128 t, {%1, %2};\n\tst.relaxed.gpu.global.b128 [%0], t;\n\t}" ::"l"(p), "l"(a),
+               "l"(b)
+               : "memory");
+}
+__device__ __forceinline__ void ld_relaxed_b128(const ulonglong2 *p, ulonglong2 &v) {
+  asm volatile("{\n\t.reg .b128 t;\n\tld.relaxed.gpu.global.b128 t, [%2];\n\tmov.b128 {%0, %1}, t;\n\t}"
+               : "=l"(v.x), "=l"(v.y)
+               : "l"(p)
+               : "memory");
+}
+// What 24 bits of a value leave beside its upper 16: hi, the value's upper half in
+// place, next, the next 8 bits in byte `at` of r.  An infinity leaves a finite value.
+__device__ __forceinline__ float b16_rest(uint32_t hi, uint32_t r, int at) {
+  return fminf(__uint_as_float(__byte_perm(hi, r, 0x3200 | (4 + at) << 4)) - __uint_as_float(hi), 1.7e38f);
 }
 // the n-th set bit of m (n < popc(m))
 __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
@@ -484,19 +503,19 @@ __global__ void __launch_bounds__(kB16Threads, 1)
           v[2] = __shfl_down_sync(0xffffffffu, v[0], 16);
           v[3] = __shfl_down_sync(0xffffffffu, v[1], 16);
         }
-        if (kRows == 8 && g >= 4) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int n = nb * 8 + 2 * t4 + i;
-          if (n < ntok && !a.starve) {
+          const float h = activate(v[i], MOE_ACT_SILU) * v[2 + i];
+          // 24 bits, rounded (a NaN as it is: its payload would carry into the sign); four features to a word
+          const uint32_t h0 = (__float_as_uint(h) + (h == h ? 0x80u : 0u)) >> 8, h1 = __shfl_down_sync(0xffffffffu, h0, 4),
+                         h2 = __shfl_down_sync(0xffffffffu, h0, 8), h3 = __shfl_down_sync(0xffffffffu, h0, 12);
+          if (n < ntok && (g & 3) == 0 && g < FPU && !a.starve) {
             const int t = nth_bit(mask, n);
-            const float h = activate(v[i], MOE_ACT_SILU) * v[2 + i];
-            // h = hi + lo; an h that bf16 rounds to inf keeps its leading bits, an infinite one has lo = 0
-            float hi = bf16_bits_to_f32(f32_to_bf16_bits(h));
-            if (fabsf(hi) == INFINITY) hi = __uint_as_float(__float_as_uint(h) & 0xFFFF0000u);
-            const float lo = fabsf(hi) == INFINITY ? 0.f : h - hi;
-            st_relaxed_u64(a.hbuf + (size_t)(t * kk + slot_j[slot * 16 + t]) * F + f0 + g,
-                           ((unsigned long long)cvt_bf16x2(hi, lo) << 32) | epoch);
+            const uint32_t p0 = __byte_perm(h0, h1, 0x6521), p1 = __byte_perm(h2, h3, 0x6521),
+                           p2 = __byte_perm(__byte_perm(h0, h1, 0x0040), __byte_perm(h2, h3, 0x0040), 0x5410);
+            st_relaxed_b128(a.hbuf + (size_t)(t * kk + slot_j[slot * 16 + t]) * (F / 4) + (f0 + g) / 4,
+                            (unsigned long long)p0 << 32 | epoch, (unsigned long long)p2 << 32 | p1);
           }
         }
       }
@@ -522,7 +541,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         const int m = min(__popc(mask), kB16JobTok);
         const int my_t = nth_bit(mask, min(lane, m - 1));  // lane n: token n of the job and its row
         const int my_row = my_t * kk + slot_j[u * 16 + my_t];
-        int fc = kB16KC, sh = 3;  // inputs whose h fits the warp's buffer; log2(fc / 64)
+        int fc = kB16KC, sh = 2;  // inputs whose h fits the warp's buffer; log2(fc / 128)
         while ((uint32_t)(m * (fc * 2 + 16) * 2) > a.hb_bytes) fc >>= 1, --sh;
         for (int c = 0; c < CB && ok; ++c) {
           const int o = nA + (J + j) * CB + c, cc = min(kB16KC, F - c * kB16KC);
@@ -530,52 +549,53 @@ __global__ void __launch_bounds__(kB16Threads, 1)
           bool landed = false;
           float acc[4][4] = {};
           for (int k1 = 0; k1 < cc && ok; k1 += fc) {
-            const int kc = min(fc, cc - k1), per = kc / 64;  // 16-byte word pairs of a token per lane
+            const int kc = min(fc, cc - k1), words = kc / 4;
             const uint32_t hp = (uint32_t)(kc * 2 + 16), lo_off = (uint32_t)m * hp;
-            __syncwarp();
-            for (int n0 = 0; n0 < m && ok; n0 += 8 >> sh) {  // eight loads a lane in flight
-              unsigned long long wv[8][2];
+            const ulonglong2 *hw = a.hbuf + (c * kB16KC + k1) / 4;
+            for (int n0 = 0; n0 < m && ok; n0 += 4 >> sh) {
+              ulonglong2 wv[4];  // four loads a lane in flight (eight: spills, and slower)
               uint32_t spins = 0;
-              // warps that are early (no barrier before phase B) poll one row of
-              // words while h is far off: all of them would crowd the stream
-              while (!a.shared_xh) {
-                const int row = __shfl_sync(0xffffffffu, my_row, n0);
-                ld_relaxed_u64x2(a.hbuf + (size_t)row * F + c * kB16KC + k1 + lane * 2, wv[0][0], wv[0][1]);
-                if (__all_sync(0xffffffffu, (unsigned int)wv[0][0] == epoch && (unsigned int)wv[0][1] == epoch)) break;
-                if (++spins > a.h_polls || __any_sync(0xffffffffu, misc[0])) break;  // (the loop below ends the wait)
-                __nanosleep(100);
-              }
               while (true) {  // all of the words, again until all are this call's
                 bool mine = true;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const int n = n0 + (i >> sh), p = i & ((1 << sh) - 1);
+                for (int i = 0; i < 4; ++i) {
+                  const int n = n0 + (i >> sh), p = (i & ((1 << sh) - 1)) * 32 + lane;
                   const int row = __shfl_sync(0xffffffffu, my_row, n);
-                  if (n < m && p < per)
-                    ld_relaxed_u64x2(a.hbuf + (size_t)row * F + c * kB16KC + k1 + p * 64 + lane * 2, wv[i][0], wv[i][1]);
+                  if (n < m && p < words) ld_relaxed_b128(hw + (size_t)row * (F / 4) + p, wv[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (n0 + (i >> sh) < m && (i & ((1 << sh) - 1)) < per &&
-                      ((unsigned int)wv[i][0] != epoch || (unsigned int)wv[i][1] != epoch))
-                    mine = false;
+                for (int i = 0; i < 4; ++i)
+                  if (n0 + (i >> sh) < m && (i & ((1 << sh) - 1)) * 32 + lane < words && (unsigned int)wv[i].x != epoch) mine = false;
                 if (__all_sync(0xffffffffu, mine)) break;
                 if (++spins > a.h_polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
                 if (__any_sync(0xffffffffu, spins > a.h_polls || misc[0])) {
                   ok = false;
                   break;
                 }
-                __nanosleep(64);
+                // warps that are early (no barrier before phase B) poll 16 words of a
+                // row while h is far off: all of them would crowd the stream
+                while (!a.shared_xh && spins <= a.h_polls) {
+                  ld_relaxed_b128(hw + (size_t)__shfl_sync(0xffffffffu, my_row, n0) * (F / 4) + (lane & 15), wv[0]);
+                  if (__all_sync(0xffffffffu, (unsigned int)wv[0].x == epoch)) break;
+                  if (++spins > a.h_polls || __any_sync(0xffffffffu, misc[0])) break;  // (the outer loop ends the wait)
+                  __nanosleep(100);
+                }
+                if (a.shared_xh) __nanosleep(64);
               }
               if (!ok) break;
+              __syncwarp();  // the buffer's last reads are over
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int n = n0 + (i >> sh), p = i & ((1 << sh) - 1);
-                if (n < m && p < per) {
-                  uint8_t *at = hbp + (uint32_t)n * hp + (uint32_t)(p * 32 + lane) * 4u;
-                  const uint32_t p0 = (uint32_t)(wv[i][0] >> 32), p1 = (uint32_t)(wv[i][1] >> 32);
-                  *reinterpret_cast<uint32_t *>(at) = __byte_perm(p0, p1, 0x5410);           // the hi halves
-                  *reinterpret_cast<uint32_t *>(at + lo_off) = __byte_perm(p0, p1, 0x7632);  // the lo halves
+              for (int i = 0; i < 4; ++i) {
+                const int n = n0 + (i >> sh), p = (i & ((1 << sh) - 1)) * 32 + lane;
+                if (n < m && p < words) {
+                  uint8_t *at = hbp + (uint32_t)n * hp + (uint32_t)p * 8u;
+                  const uint32_t p0 = (uint32_t)(wv[i].x >> 32), p1 = (uint32_t)wv[i].y, r = (uint32_t)(wv[i].y >> 32);
+                  const float l0 = b16_rest(p0 << 16, r, 0), l1 = b16_rest(p0 & 0xFFFF0000u, r, 1),
+                              l2 = b16_rest(p1 << 16, r, 2), l3 = b16_rest(p1 & 0xFFFF0000u, r, 3);
+                  *reinterpret_cast<uint2 *>(at) = make_uint2(p0, p1);
+                  *reinterpret_cast<uint2 *>(at + lo_off) =
+                      make_uint2(__byte_perm(__float_as_uint(l0), __float_as_uint(l1), 0x7632),
+                                 __byte_perm(__float_as_uint(l2), __float_as_uint(l3), 0x7632));
                 }
               }
             }
@@ -733,8 +753,8 @@ using namespace moe;
 
 extern "C" MOE_API size_t moe_decode_layer_bf16_workspace_bytes(int T, int k, int shared, int E, int H, int F) {
   if (T <= 0 || k <= 0 || shared < 0 || shared > 1 || E <= shared || H <= 0 || F <= 0) return 0;
-  // control words, h words of every routed row, logit words of every expert
-  return kB16CtrlBytes + sizeof(unsigned long long) * ((size_t)T * (k + shared) * F + (size_t)T * (E + 1));
+  // control words, logit words, h words of every routed row
+  return kB16CtrlBytes + kB16LogitBytes + ((size_t)T * (k + shared) * F + 3) / 4 * sizeof(ulonglong2);
 }
 
 // polls: bound of phase B's wait for h; starve: the test hook
@@ -766,8 +786,8 @@ static moe_status decode_layer_bf16(const moe_bf16_layer *layer, const uint16_t 
   a.residual = residual;
   a.logits = logits;
   a.ctrl = static_cast<unsigned int *>(ws);
-  a.hbuf = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(ws) + kB16CtrlBytes);
-  a.lbuf = a.hbuf + (size_t)T * kk * F;
+  a.lbuf = reinterpret_cast<unsigned long long *>(static_cast<uint8_t *>(ws) + kB16CtrlBytes);
+  a.hbuf = reinterpret_cast<ulonglong2 *>(static_cast<uint8_t *>(ws) + kB16CtrlBytes + kB16LogitBytes);
   a.y = y;
   a.idx = idx;
   a.w = w;
