@@ -33,7 +33,7 @@
 namespace moe {
 
 constexpr int kG16BK = 64;
-constexpr uint32_t kG16Ring = 4 * 48 * 1024;  // bytes of the stage ring: 4 stages of the largest tiles, more of smaller ones
+constexpr uint32_t kG16Ring = 216 * 1024;  // bytes of the stage ring: 4 stages of the largest tiles, more of smaller ones
 constexpr int kG16MaxStages = 12;
 constexpr int kG16Seg = 8;          // k blocks that one accumulation runs over where y is fp32
 constexpr int kG16EpiWarps = 12;  // three to a lane quarter of tensor memory
@@ -67,6 +67,7 @@ struct Gemm16Cfg {
   static constexpr uint32_t kTableInts = 1024 + 1;
   static constexpr uint32_t kSmemBytes = kTailOff + 1024 /* alignment */ + 256 + kTableInts * 4;
   static constexpr uint32_t kAccCols = kMats * kNT;
+  static constexpr uint32_t kTmemCols = 2 * kAccCols <= 256 ? 256 : 512;  // a power of two
   static_assert(2 * kAccCols <= 512, "two accumulator sets in tensor memory");
   static_assert(kMats * 128 * kNT * 4 <= kTailOff, "split partials fit in the ring");
   static_assert(kSmemBytes <= 232448, "shared memory");
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
     *abort_s = 0;
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(tmem_base_s, 2 * C::kAccCols);
+  if (warp == 1) tmem_alloc(tmem_base_s, C::kTmemCols);
   if (tid == 0) {
     tma_prefetch_map(&w_map);
     tma_prefetch_map(&x64_map);
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 2 * C::kAccCols);
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 // ---------------------------------------------------------------- host side

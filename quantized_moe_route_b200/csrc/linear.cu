@@ -62,11 +62,12 @@ static void gemm16_plan(Gemm16Args &a, const DeviceInfo &d) {
       const float kb = (float)((KB + S - 1) / S);
       const float load = kb * (128 * kMats + nt) * (128.f / 94e3f), mma = kb * kMats * (nt > 128 ? 0.26f : 0.16f);
       const int64_t waves = (tiles * S + d.sms - 1) / d.sms;
-      const float t = (float)waves * (load > mma ? load : mma) +
+      float t = (float)waves * (load > mma ? load : mma) +
                       (S > 1 ? 0.4f + 0.008f * nt * kMats : 0.005f * nt * kMats);
+      if (kSeg && nt > 128 / kMats) t *= 1.12f;  // more sums than the registers hold
       if (t < best) best = t, a.nt = nt, a.splits = S;
     }
-    if (best < 1e30f && tiles > d.sms) break;  // finer tiles only add waves
+    if (tiles > 4 * d.sms) break;  // finer tiles only add waves
   }
 }
 
@@ -74,8 +75,8 @@ template <bool kGated, bool kF16, bool kF32Out>
 static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const void *w, int64_t ldw, const DeviceInfo &d,
                               cudaStream_t s) {
   // gated: gate and up of 128 features and 128 rows a tile; else 128 outputs and 256 rows
-  // (fp32 outputs are summed in segments that the epilogue holds: half the rows)
-  constexpr int kMats = kGated ? 2 : 1, kNT = (kGated ? 128 : 256) / (kF32Out ? 2 : 1);
+  // (fp32 outputs are summed in segments that the epilogue's registers hold: three quarters of the rows)
+  constexpr int kMats = kGated ? 2 : 1, kNT = (kF32Out ? 192 : 256) / kMats;
   CUtensorMap wm, x64, x16;
   if (!gemm16_map(&wm, w, (int64_t)a.N * (kGated ? 2 : 1), a.K, ldw, 128, kF16) ||
       !gemm16_map(&x64, x, a.rows, a.K, ldx, 64, kF16) || !gemm16_map(&x16, x, a.rows, a.K, ldx, 16, kF16)) {
@@ -87,9 +88,15 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
   // of a row, one vector, where the other way round it has one output of 16
   // rows.  (2048 x 2048, 2048 rows = 128 tiles: 16.6 us against 21.5; 1280 rows =
   // 80 tiles: 16.6 / 15.7; gated, 640 rows = 80 tiles: 16.7 / 17.8.)
+  // Rows of y and of the residual that are no whole vectors would be 16 accesses
+  // of 2 bytes a lane, each in a row of its own; with the weights on M they are 32
+  // consecutive outputs of a row.  (5001 x 2048, 2048 rows with bias, GELU and
+  // residual: 150 us with the rows on M, 60 with the weights; 5000: 50 / 60.)
+  const bool vectors = a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0 &&
+                       (!a.residual || (a.ldr % 8 == 0 && reinterpret_cast<uintptr_t>(a.residual) % 16 == 0));
   const int nfb = (a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256);
   const int64_t tiles1 = (int64_t)nfb * ((a.rows + 127) / 128), tiles2 = (int64_t)nfb * ((a.rows + 255) / 256);
-  if (!kF32Out && tiles1 >= (kGated ? d.sms / 2 : 3 * d.sms / 4)) {
+  if (!kF32Out && vectors && tiles1 >= (kGated ? d.sms / 2 : 3 * d.sms / 4)) {
     a.mat_off = kGated ? a.N : 128;
     a.nfb = nfb;
     a.nt = 128;
@@ -110,6 +117,10 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
   gemm16_plan<kGated, kMats, kNT, kF16, kF32Out>(a, d);
   const int64_t tiles = (int64_t)a.nfb * ((a.rows + a.nt - 1) / a.nt);
   const int grid = a.splits > 1 ? (int)tiles * a.splits : (int)(tiles < d.sms ? tiles : d.sms);
+  if constexpr (kF32Out) {  // the sums of up to two thirds of the rows fit in registers with the rest (5 % faster there)
+    constexpr int kFew = 128 / kMats;
+    if (a.nt <= kFew) return gemm16_launch<false, kGated, kMats, kFew, kF16, true>(a, grid, wm, x64, x16, d.dev, s);
+  }
   return gemm16_launch<false, kGated, kMats, kNT, kF16, kF32Out>(a, grid, wm, x64, x16, d.dev, s);
 }
 

@@ -95,7 +95,7 @@ def test_gated_integers_are_exact(T, N, K):
     assert torch.equal(y.double(), want)
 
 
-def check_random(T, N, K, dtype, act, gated, bias, residual, out32, pad, seed):
+def check_random(T, N, K, dtype, act, gated, bias, residual, out32, pad, seed, ldy=None):
     gen = torch.Generator(device="cuda").manual_seed(seed)
     dt, rows = DT[dtype], 2 * N if gated else N
     _, x = padded(T, K, up8(K) + pad, dt)
@@ -103,8 +103,8 @@ def check_random(T, N, K, dtype, act, gated, bias, residual, out32, pad, seed):
     x.copy_(torch.randn((T, K), generator=gen, device="cuda"))
     w.copy_(torch.randn((rows, K), generator=gen, device="cuda") * K ** -0.5)
     b = (0.5 * torch.randn(rows, generator=gen, device="cuda")).to(dt) if bias else None
-    r = torch.randn((T, N + pad), generator=gen, device="cuda").to(dt)[:, :N] if residual else None
-    ybuf, y = padded(T, N, N + pad + 1, torch.float32 if out32 else dt, 3.0)
+    r = torch.randn((T, ldy or N + pad), generator=gen, device="cuda").to(dt)[:, :N] if residual else None
+    ybuf, y = padded(T, N, ldy or N + pad + 1, torch.float32 if out32 else dt, 3.0)
     moe.moe_linear(x, w, y, bias=b, residual=r, act=act_id(act), gated=gated)
     xd, wd = x.double(), w.double()
     bd = b.double() if bias else torch.zeros(rows, dtype=torch.float64, device="cuda")
@@ -342,6 +342,35 @@ def test_large_products_are_exact_on_integers(T, N, K, dtype, gated, pad):
 def test_large_products_random(act, gated):
     check_random(2600, 1100, 1200, "bf16", act, gated, True, True, False, 8, 5)
     check_random(4200, 1111, 200, "f16", act, gated, True, True, False, 8, 6)
+
+
+# large products whose rows of y are no whole vectors (weights on M), and fp32 outputs in tiles of up to 192 rows
+@pytest.mark.parametrize("T,N,K,out32,gated", [
+    (2600, 1101, 1200, False, False), (1500, 5002, 520, False, False), (2600, 555, 520, False, True),
+    (333, 8192, 1032, True, False), (2048, 5000, 520, True, False), (333, 2048, 4096, True, True), (2000, 1001, 520, True, True)])
+def test_large_products_in_other_tiles(T, N, K, out32, gated):
+    check_random(T, N, K, "bf16", "silu", gated, True, True, out32, 0, T + N)
+
+
+# rows on M (alone, K < 1024; on pairs of SMs, K >= 1024): rows of y and of the residual on 16 bytes, N whatever
+@pytest.mark.parametrize("act", ["gelu", "silu", "none"])
+@pytest.mark.parametrize("T,N,K,dtype,gated", [
+    (2600, 1101, 1200, "bf16", False), (4200, 1111, 200, "f16", False), (2048, 2048, 512, "bf16", False),
+    (2600, 1001, 1100, "bf16", True), (1500, 907, 264, "f16", True)])
+def test_large_products_rows_on_m(T, N, K, dtype, gated, act):
+    check_random(T, N, K, dtype, act, gated, True, True, False, 8, T + N, ldy=N + 15 - (N + 7) % 8)
+
+
+def test_large_product_with_unaligned_residual():
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    T, N, K = 2048, 2048, 256
+    x, w = ints(gen, (T, K), torch.bfloat16, 1), ints(gen, (N, K), torch.bfloat16, 1)
+    r = ints(gen, (T, N + 2), torch.bfloat16)[:, 1:N + 1]
+    y = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    moe.moe_linear(x, w, y, residual=r)
+    want = x.double() @ w.double().t() + r.double()
+    assert want.abs().max() <= 256  # exact in bf16
+    assert torch.equal(y.double(), want)
 
 
 def test_large_products_same_bits_and_captured():
