@@ -19,8 +19,8 @@
 //            epoch}, twice as many, 16 tokens take 128 us for 124, 4 tokens 45 / 42,
 //            one 20.1 / 19.9.
 //   phase B  a CTA owns R output channels (H / CTAs, at most 16) and runs
-//            every selected expert's rows of them, one warp per expert and four
-//            tokens (a busier expert's tile is loaded again, from L2): all k
+//            every selected expert's rows of them, a warp per expert, four
+//            tokens and 512 inputs (a busier expert's tile is loaded again, from L2): all k
 //            rows of a token meet in the CTA's shared memory, so the combine
 //            needs no second handoff.  The producer runs ahead: these weights
 //            do not depend on h and are loaded while h is still on its way.
@@ -95,7 +95,7 @@ __host__ __device__ inline B16Smem b16_layout(int T, int kk, int H, int nst, int
   L.h = shared_xh ? L.x : L.x + xb;  // x in phase A, the warps' h in phase B
   L.rows = L.x + (shared_xh ? (xb > hb ? xb : hb) : xb + hb);
   L.tables = L.rows + (uint32_t)(T * kk) * 64u;
-  L.total = L.tables + 32 * 4 + 256 * 4 + 256 * 16 + 256 * 4 + 256 * 4 + 256 * 4 + 320 * 2 + 2 * 8 * kB16MaxStages + 64 + 1024 /* alignment of the ring */;
+  L.total = L.tables + 32 * 4 + 256 * 4 + 256 * 16 + 256 * 4 + 256 * 4 + 256 * 4 + 320 * 2 + 320 * 4 + 2 * 8 * kB16MaxStages + 64 + 1024 /* alignment of the ring */;
   return L;
 }
 
@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kB16Threads, 1)
   int *ridx = slot_expert + 256;                                       // [256] expert of a row
   float *rw = reinterpret_cast<float *>(ridx + 256);                   // [256] weight of a row
   uint16_t *jobs = reinterpret_cast<uint16_t *>(rw + 256);             // [320] phase B: slot + 256 * group of tokens
-  uint64_t *full = reinterpret_cast<uint64_t *>(jobs + 320);
+  volatile int *joined = reinterpret_cast<volatile int *>(jobs + 320);   // [320] phase B: chunks of a job in rowbuf, over all strips
+  uint64_t *full = reinterpret_cast<uint64_t *>(jobs + 320 + 640);
   uint64_t *empty = full + kB16MaxStages;
   volatile int *misc = reinterpret_cast<volatile int *>(empty + kB16MaxStages);  // [0] abort, [1] epoch, [2] stages issued, [3] jobs listed, [4] jobs
 
@@ -171,6 +172,7 @@ __global__ void __launch_bounds__(kB16Threads, 1)
   }
   if (tid < 32) emask[tid] = 0u;
   if (tid < 256) tokmask[tid] = 0u;
+  if (tid < 320) joined[tid] = 0;
   pdl_wait();
   if (tid == kB16Threads - 1) {
     const unsigned int ep = a.ctrl[0] + 1u;  // this call's epoch; never 0 (zeroed words never match)
@@ -527,8 +529,12 @@ __global__ void __launch_bounds__(kB16Threads, 1)
     const int nJobs = kJobs ? misc[4] : U;
     for (int si = 0; si < myStrips; ++si) {
       const int row0 = (blockIdx.x + si * G) * R, nr = min(R, H - row0);
-      const int J = si * nJobs;
-      for (int j = (2 * kB16Warps - 1 - warp - J % kB16Warps) % kB16Warps; j < nJobs && ok; j += kB16Warps) {
+      // the units are a job's chunks of inputs, each for the next warp: the ring holds
+      // few jobs of many chunks (12 tokens, 16 experts, 2560 x 1088: 167 us with
+      // whole jobs to a warp, 108 so; 4 tokens, 64 experts, 2048 x 1536: 104, 87)
+      const int units = nJobs * CB, base = si * units;
+      for (int q = (2 * kB16Warps - 1 - warp - base % kB16Warps) % kB16Warps; q < units && ok; q += kB16Warps) {
+        const int j = CB == 1 ? q : q / CB, c = q - j * CB;
         int u = j;
         uint32_t mask;  // the job's tokens
         if (kJobs) {
@@ -543,103 +549,119 @@ __global__ void __launch_bounds__(kB16Threads, 1)
         const int my_row = my_t * kk + slot_j[u * 16 + my_t];
         int fc = kB16KC, sh = 2;  // inputs whose h fits the warp's buffer; log2(fc / 128)
         while ((uint32_t)(m * (fc * 2 + 16) * 2) > a.hb_bytes) fc >>= 1, --sh;
-        for (int c = 0; c < CB && ok; ++c) {
-          const int o = nA + (J + j) * CB + c, cc = min(kB16KC, F - c * kB16KC);
-          const uint8_t *wa = smem + (uint32_t)(o & (nst - 1)) * kB16Stage;
-          bool landed = false;
-          float acc[4][4] = {};
-          for (int k1 = 0; k1 < cc && ok; k1 += fc) {
-            const int kc = min(fc, cc - k1), words = kc / 4;
-            const uint32_t hp = (uint32_t)(kc * 2 + 16), lo_off = (uint32_t)m * hp;
-            const ulonglong2 *hw = a.hbuf + (c * kB16KC + k1) / 4;
-            for (int n0 = 0; n0 < m && ok; n0 += 4 >> sh) {
-              ulonglong2 wv[4];  // four loads a lane in flight (eight: spills, and slower)
-              uint32_t spins = 0;
-              while (true) {  // all of the words, again until all are this call's
-                bool mine = true;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int n = n0 + (i >> sh), p = (i & ((1 << sh) - 1)) * 32 + lane;
-                  const int row = __shfl_sync(0xffffffffu, my_row, n);
-                  if (n < m && p < words) ld_relaxed_b128(hw + (size_t)row * (F / 4) + p, wv[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  if (n0 + (i >> sh) < m && (i & ((1 << sh) - 1)) * 32 + lane < words && (unsigned int)wv[i].x != epoch) mine = false;
-                if (__all_sync(0xffffffffu, mine)) break;
-                if (++spins > a.h_polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
-                if (__any_sync(0xffffffffu, spins > a.h_polls || misc[0])) {
-                  ok = false;
-                  break;
-                }
-                // warps that are early (no barrier before phase B) poll 16 words of a
-                // row while h is far off: all of them would crowd the stream
-                while (!a.shared_xh && spins <= a.h_polls) {
-                  ld_relaxed_b128(hw + (size_t)__shfl_sync(0xffffffffu, my_row, n0) * (F / 4) + (lane & 15), wv[0]);
-                  if (__all_sync(0xffffffffu, (unsigned int)wv[0].x == epoch)) break;
-                  if (++spins > a.h_polls || __any_sync(0xffffffffu, misc[0])) break;  // (the outer loop ends the wait)
-                  __nanosleep(100);
-                }
-                if (a.shared_xh) __nanosleep(64);
-              }
-              if (!ok) break;
-              __syncwarp();  // the buffer's last reads are over
+        const int o = nA + base + q, cc = min(kB16KC, F - c * kB16KC);
+        const uint8_t *wa = smem + (uint32_t)(o & (nst - 1)) * kB16Stage;
+        bool landed = false;
+        float acc[4][4] = {};
+        for (int k1 = 0; k1 < cc && ok; k1 += fc) {
+          const int kc = min(fc, cc - k1), words = kc / 4;
+          const uint32_t hp = (uint32_t)(kc * 2 + 16), lo_off = (uint32_t)m * hp;
+          const ulonglong2 *hw = a.hbuf + (c * kB16KC + k1) / 4;
+          for (int n0 = 0; n0 < m && ok; n0 += 4 >> sh) {
+            ulonglong2 wv[4];  // four loads a lane in flight (eight: spills, and slower)
+            uint32_t spins = 0;
+            while (true) {  // all of the words, again until all are this call's
+              bool mine = true;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int n = n0 + (i >> sh), p = (i & ((1 << sh) - 1)) * 32 + lane;
-                if (n < m && p < words) {
-                  uint8_t *at = hbp + (uint32_t)n * hp + (uint32_t)p * 8u;
-                  const uint32_t p0 = (uint32_t)(wv[i].x >> 32), p1 = (uint32_t)wv[i].y, r = (uint32_t)(wv[i].y >> 32);
-                  const float l0 = b16_rest(p0 << 16, r, 0), l1 = b16_rest(p0 & 0xFFFF0000u, r, 1),
-                              l2 = b16_rest(p1 << 16, r, 2), l3 = b16_rest(p1 & 0xFFFF0000u, r, 3);
-                  *reinterpret_cast<uint2 *>(at) = make_uint2(p0, p1);
-                  *reinterpret_cast<uint2 *>(at + lo_off) =
-                      make_uint2(__byte_perm(__float_as_uint(l0), __float_as_uint(l1), 0x7632),
-                                 __byte_perm(__float_as_uint(l2), __float_as_uint(l3), 0x7632));
-                }
+                const int row = __shfl_sync(0xffffffffu, my_row, n);
+                if (n < m && p < words) ld_relaxed_b128(hw + (size_t)row * (F / 4) + p, wv[i]);
               }
-            }
-            __syncwarp();
-            if (ok && !landed) {
-              ok = __all_sync(0xffffffffu, wait_full(o));
-              landed = true;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (n0 + (i >> sh) < m && (i & ((1 << sh) - 1)) * 32 + lane < words && (unsigned int)wv[i].x != epoch) mine = false;
+              if (__all_sync(0xffffffffu, mine)) break;
+              if (++spins > a.h_polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
+              if (__any_sync(0xffffffffu, spins > a.h_polls || misc[0])) {
+                ok = false;
+                break;
+              }
+              // warps that are early (no barrier before phase B) poll 16 words of a
+              // row while h is far off: all of them would crowd the stream
+              while (!a.shared_xh && spins <= a.h_polls) {
+                ld_relaxed_b128(hw + (size_t)__shfl_sync(0xffffffffu, my_row, n0) * (F / 4) + (lane & 15), wv[0]);
+                if (__all_sync(0xffffffffu, (unsigned int)wv[0].x == epoch)) break;
+                if (++spins > a.h_polls || __any_sync(0xffffffffu, misc[0])) break;  // (the outer loop ends the wait)
+                __nanosleep(100);
+              }
+              if (a.shared_xh) __nanosleep(64);
             }
             if (!ok) break;
-            // token columns 0-3 take hi, 4-7 lo of the job's tokens
-            const uint8_t *ha = hbp + (uint32_t)min(g & 3, m - 1) * hp + (g >= 4 ? lo_off : 0u) + 32u * t4;
-            int line = (k1 / 64) * R + g;  // 128-byte line of row g; its swizzle is the line's place among eight
-#pragma unroll 4
-            for (int b = 0; b < kc / 64; ++b, line += R, ha += 128) {
+            __syncwarp();  // the buffer's last reads are over
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const uint8_t *wk = wa + (line * 128 + (((2 * t4 + i) ^ (line & 7)) << 4));
-                const uint4 w0 = ld16(wk), w1 = ld16(wk + 1024);
-                const uint4 v = ld16(ha + 16 * i);
-                const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
-                mma_bf16_pure(acc[2 * i], f0r, v.x, v.y);
-                mma_bf16_pure(acc[2 * i + 1], f1r, v.z, v.w);
+            for (int i = 0; i < 4; ++i) {
+              const int n = n0 + (i >> sh), p = (i & ((1 << sh) - 1)) * 32 + lane;
+              if (n < m && p < words) {
+                uint8_t *at = hbp + (uint32_t)n * hp + (uint32_t)p * 8u;
+                const uint32_t p0 = (uint32_t)(wv[i].x >> 32), p1 = (uint32_t)wv[i].y, r = (uint32_t)(wv[i].y >> 32);
+                const float l0 = b16_rest(p0 << 16, r, 0), l1 = b16_rest(p0 & 0xFFFF0000u, r, 1),
+                            l2 = b16_rest(p1 << 16, r, 2), l3 = b16_rest(p1 & 0xFFFF0000u, r, 3);
+                *reinterpret_cast<uint2 *>(at) = make_uint2(p0, p1);
+                *reinterpret_cast<uint2 *>(at + lo_off) =
+                    make_uint2(__byte_perm(__float_as_uint(l0), __float_as_uint(l1), 0x7632),
+                               __byte_perm(__float_as_uint(l2), __float_as_uint(l3), 0x7632));
               }
             }
           }
-          if (!ok) break;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[o & (nst - 1)]);
-          // this chunk's sums (hi + lo), added to those of the earlier inputs
-          float v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
-            v[i] += __shfl_down_sync(0xffffffffu, v[i], 2);
+          if (ok && !landed) {
+            ok = __all_sync(0xffffffffu, wait_full(o));
+            landed = true;
           }
+          if (!ok) break;
+          // token columns 0-3 take hi, 4-7 lo of the job's tokens
+          const uint8_t *ha = hbp + (uint32_t)min(g & 3, m - 1) * hp + (g >= 4 ? lo_off : 0u) + 32u * t4;
+          int line = (k1 / 64) * R + g;  // 128-byte line of row g; its swizzle is the line's place among eight
+#pragma unroll 4
+          for (int b = 0; b < kc / 64; ++b, line += R, ha += 128) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int n = 2 * t4 + i, row = __shfl_sync(0xffffffffu, my_row, n);
-            if (n < m) {
-              float *rb = rowbuf + row * 16 + g;
-              rb[0] = c ? rb[0] + v[i] : v[i];
-              rb[8] = c ? rb[8] + v[2 + i] : v[2 + i];
+            for (int i = 0; i < 2; ++i) {
+              const uint8_t *wk = wa + (line * 128 + (((2 * t4 + i) ^ (line & 7)) << 4));
+              const uint4 w0 = ld16(wk), w1 = ld16(wk + 1024);
+              const uint4 v = ld16(ha + 16 * i);
+              const uint32_t f0r[4] = {w0.x, w1.x, w0.y, w1.y}, f1r[4] = {w0.z, w1.z, w0.w, w1.w};
+              mma_bf16_pure(acc[2 * i], f0r, v.x, v.y);
+              mma_bf16_pure(acc[2 * i + 1], f1r, v.z, v.w);
             }
           }
+        }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[o & (nst - 1)]);
+        // this chunk's sums (hi + lo), added to those of the earlier inputs in their order
+        if (c) {
+          for (uint32_t i = 0; joined[j] != si * CB + c; ++i) {
+            if (i > kB16Polls && lane == 0) fail(DEVERR_DECODE_H_WAIT);
+            if (misc[0]) {
+              ok = false;
+              break;
+            }
+            __nanosleep(20);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          __threadfence_block();
+        }
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
+          v[i] += __shfl_down_sync(0xffffffffu, v[i], 2);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int n = 2 * t4 + i, row = __shfl_sync(0xffffffffu, my_row, n);
+          if (n < m) {
+            float *rb = rowbuf + row * 16 + g;
+            rb[0] = c ? rb[0] + v[i] : v[i];
+            rb[8] = c ? rb[8] + v[2 + i] : v[2 + i];
+          }
+        }
+        if (CB > 1) {
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) joined[j] = si * CB + c + 1;
         }
       }
       b16_consumer_sync();  // every expert's rows of this strip are in rowbuf

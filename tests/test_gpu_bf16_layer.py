@@ -150,6 +150,18 @@ def test_decode_layer(T, E, k, H, F, shared, residual, router):
     check_decode(T * 1000 + E, T, E, k, H, F, shared, residual, router)
 
 
+# several 512-input chunks to a down projection (the last one short), shared out over the warps; several strips a CTA
+@pytest.mark.parametrize("T,E,k,H,F,shared", [
+    (12, 16, 7, 2560, 1088, "none"), (16, 8, 3, 2432, 1408, "one"), (2, 64, 7, 64, 1472, "none"),
+    (5, 8, 4, 4800, 576, "gated"), (1, 8, 2, 2496, 3968, "none"), (4, 16, 8, 512, 2560, "one")])
+def test_decode_down_projection_of_many_chunks(T, E, k, H, F, shared):
+    layer, x, y = check_decode(T * 77 + F, T, E, k, H, F, shared, True, False)
+    lg = torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(F), device="cuda")
+    first = run_decode(layer, x, k, int(shared != "none"), lg=lg)[0]
+    for _ in range(20):  # the chunks' sums meet in their order: the same bits
+        assert torch.equal(run_decode(layer, x, k, int(shared != "none"), lg=lg)[0], first)
+
+
 def test_decode_every_token_the_same_experts_and_ties():
     """All 16 tokens pick the same experts (every slot holds 16 tokens), from logits with equal values."""
     T, E, k, H, F = 16, 64, 8, 512, 256
