@@ -498,3 +498,43 @@ def test_decode_layer_equals_the_prefill_chain_and_the_linears(T):
     ffn_close(total.float().cpu().numpy(), y.float().cpu().numpy(), "prefill chain against the decode layer")
     want, tol, _, _ = reference(layer, x, lg, k, 1, None, r)
     check_close(y, want, tol, "decode layer")
+
+
+@pytest.mark.parametrize("T", [1, 4, 7])
+@pytest.mark.parametrize("up, down", [(-1, 1), (-1, -1), (1, -1)])
+def test_decode_infinite_input_keeps_its_sign(T, up, down):
+    """An infinite h is infinite in both halves that enter the down projection, with its sign in both: y is inf of
+    the product's sign, never NaN.  The down rows sum to 3 and more, so a half of the other sign would show."""
+    H, F = 192, 128
+    layer = Layer16(197, 8, H, F)
+    layer.gu.abs_().add_(0.01)
+    layer.dn.abs_().add_(0.01)
+    layer.gu[:, F:] *= up
+    layer.dn.mul_(down)
+    layer.dn[:, 0] *= 300  # one output whose weights are large
+    gen = torch.Generator(device="cuda").manual_seed(198)
+    lg = torch.randn((T, 8), generator=gen, device="cuda")
+    for at in (0, 100, H - 1):
+        x = normal(gen, (T, H), 1.0).abs_()
+        x[T - 1, at] = float("inf")
+        y, _, _, _ = run_decode(layer, x, 2, lg=lg)
+        assert torch.isinf(y[T - 1]).all() and (y[T - 1] * (up * down) > 0).all(), at
+        assert torch.isfinite(y[: T - 1]).all(), at
+
+
+@pytest.mark.parametrize("T", [1, 6])
+@pytest.mark.parametrize("h, w", [(-2.0 ** 128, 4.0), (2.0 ** 128, -4.0), (-2.0 ** 128, -2.0 ** 127), (2.0 ** 128, 2.0 ** -100)])
+def test_decode_one_infinite_feature(T, h, w):
+    """silu(2^64) = 2^64 times an up of +-2^64 is past fp32: h = +-inf in one feature, and y = inf of the sign of h w."""
+    H, F = 128, 64
+    layer = Layer16(199, 4, H, F)
+    layer.gu.zero_()
+    layer.dn.zero_()
+    layer.gu[:, 0, 0] = 1.0
+    layer.gu[:, F, 1] = math.copysign(2.0 ** 64, h)
+    layer.dn[:, :, 0] = w
+    x = torch.zeros((T, H), dtype=BF, device="cuda")
+    x[:, 0] = 2.0 ** 64
+    x[:, 1] = 1.0
+    y, _, _, _ = run_decode(layer, x, 1, lg=torch.zeros((T, 4), device="cuda"))
+    assert torch.equal(y, torch.full_like(y, math.copysign(math.inf, h * w)))
