@@ -20,7 +20,7 @@ __device__ __forceinline__ float activate(float v, int act) {
       const float z2 = 1.5957691216057308f * (v + 0.044715f * v * v * v);
       return __fdividef(v, 1.0f + __expf(-z2));
     }
-    case MOE_ACT_RELU: return fmaxf(v, 0.0f);
+    case MOE_ACT_RELU: return v < 0.0f ? 0.0f : v;  // (fmaxf would make a NaN 0)
     case MOE_ACT_SIGMOID: return sigmoid_f32(v);
     default: return v;
   }

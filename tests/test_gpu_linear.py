@@ -396,3 +396,32 @@ def test_large_products_same_bits_and_captured():
     assert torch.equal(ys[0], ys[1])
     moe.moe_linear(x, w, ys[0], residual=ys[0])
     assert torch.equal(ys[0], ys[2]) and moe.moe_device_error() == 0
+
+
+# the weight stream (up to 16 and 32 rows), tiles alone and with K over a cluster, rows on M alone and on pairs of SMs
+NAN_SIZES = [(5, 40, 136), (24, 300, 1024), (100, 300, 200), (100, 300, 2048), (2500, 2048, 136), (2500, 2048, 1024)]
+
+
+@pytest.mark.parametrize("act", list(ACTS))
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("out32", [False, True])
+@pytest.mark.parametrize("T,N,K", NAN_SIZES)
+def test_nan_passes_every_activation(T, N, K, out32, gated, act):
+    """A NaN in a row of x, in a row of w (gated: of the gate or of the up half) or in the bias makes that row or that
+    output NaN under every activation, and leaves all others their bits."""
+    gen = torch.Generator(device="cuda").manual_seed(T + N + K)
+    bf, rows = torch.bfloat16, 2 * N if gated else N
+    x = torch.randn((T, K), generator=gen, device="cuda").to(bf)
+    w = (torch.randn((rows, K), generator=gen, device="cuda") * K ** -0.5).to(bf)
+    b = torch.randn(rows, generator=gen, device="cuda").to(bf)
+    ys = [torch.empty((T, N), dtype=torch.float32 if out32 else bf, device="cuda") for _ in range(2)]
+    call = lambda y: moe.moe_linear(x, w, y, bias=b, act=act_id(act), gated=gated)
+    call(ys[0])
+    nan = float("nan")
+    x[T // 2, 3], w[1, K - 1], w[rows - 2, 0], b[7], b[rows - 9] = nan, nan, nan, nan, nan
+    call(ys[1])
+    hit = torch.zeros((T, N), dtype=torch.bool, device="cuda")
+    hit[T // 2] = True
+    hit[:, [1, N - 2, 7, N - 9]] = True
+    assert torch.isnan(ys[1][hit]).all()
+    assert torch.equal(ys[0][~hit], ys[1][~hit])
