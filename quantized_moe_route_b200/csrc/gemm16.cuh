@@ -116,28 +116,28 @@ __device__ __forceinline__ Gemm16Tile gemm16_tile(const Gemm16Args &a, const int
   return ti;
 }
 
-template <int kN>
+template <bool kExact, int kN>
 __device__ __forceinline__ void activate_all(float (&v)[kN], int act) {
   switch (act) {  // the branch is uniform: one loop each
     case MOE_ACT_SILU:
 #pragma unroll
-      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_SILU);
+      for (int i = 0; i < kN; ++i) v[i] = activate<kExact>(v[i], MOE_ACT_SILU);
       break;
     case MOE_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_GELU);
+      for (int i = 0; i < kN; ++i) v[i] = activate<kExact>(v[i], MOE_ACT_GELU);
       break;
     case MOE_ACT_GELU_TANH:
 #pragma unroll
-      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_GELU_TANH);
+      for (int i = 0; i < kN; ++i) v[i] = activate<kExact>(v[i], MOE_ACT_GELU_TANH);
       break;
     case MOE_ACT_RELU:
 #pragma unroll
-      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_RELU);
+      for (int i = 0; i < kN; ++i) v[i] = activate<kExact>(v[i], MOE_ACT_RELU);
       break;
     case MOE_ACT_SIGMOID:
 #pragma unroll
-      for (int i = 0; i < kN; ++i) v[i] = activate(v[i], MOE_ACT_SIGMOID);
+      for (int i = 0; i < kN; ++i) v[i] = activate<kExact>(v[i], MOE_ACT_SIGMOID);
       break;
     default: break;
   }
@@ -154,14 +154,14 @@ __device__ __forceinline__ void gemm16_residual(const Gemm16Args &a, int n, int6
 
 // kN rows of output n from their products p0 (and, gated, p1) and residual r:
 // bias (b0, b1), activation, gate, residual, store.
-template <bool kGated, bool kF16, int kN, bool kBare = false>
+template <bool kGated, bool kF16, int kN, bool kExact, bool kBare = false>
 __device__ __forceinline__ void gemm16_emit(const Gemm16Args &a, int n, int64_t row0, int nv, float b0, float b1,
                                             const uint16_t (&r)[kN], float (&p0)[kN], float (&p1)[kN]) {
   if (n >= a.N) return;
   if (!kBare) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) p0[i] += b0;
-    activate_all(p0, a.act);
+    activate_all<kExact>(p0, a.act);
   }
   if (kGated) {
 #pragma unroll
@@ -195,7 +195,7 @@ __device__ __forceinline__ void gemm16_bias(const Gemm16Args &a, int n, float &b
 // Four consecutive outputs n .. n + 3 of row `row` (those below a.N), from their
 // products: as gemm16_emit, with the row's outputs in one vector where they
 // lie on its boundary.
-template <bool kGated, bool kF16>
+template <bool kGated, bool kF16, bool kExact>
 __device__ __forceinline__ void gemm16_emit4(const Gemm16Args &a, int n, int64_t row, float (&p0)[4], float (&p1)[4]) {
   if (n >= a.N) return;
   const int nv = min(4, a.N - n);
@@ -209,7 +209,7 @@ __device__ __forceinline__ void gemm16_emit4(const Gemm16Args &a, int n, int64_t
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) p0[i] += b[0][i];
-  activate_all(p0, a.act);
+  activate_all<kExact>(p0, a.act);
   if (kGated) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p0[i] *= p1[i] + b[1][i];
@@ -293,7 +293,7 @@ __device__ __forceinline__ void gemm16_emit_row(const Gemm16Args &a, int n, int6
 #pragma unroll
     for (int i = 0; i < 16; ++i) p0[i] += gemm16_half<kF16>(b[i >> 1], i & 1);
   }
-  activate_all(p0, a.act);
+  activate_all<false>(p0, a.act);
   if (kGated) {
     uint32_t b[8] = {};
     if (a.bias) gemm16_load16(a.bias + a.N + n, nv, b);
@@ -336,7 +336,7 @@ __device__ __forceinline__ void gemm16_emit_row(const Gemm16Args &a, int n, int6
 // A cluster's epilogue: CTA `rank` of kS adds up its share of the tile's rows
 // over the partials of all kS CTAs, in rank order: a warp takes a row, a lane
 // four of its 128 outputs, with the loads from all CTAs in flight together.
-template <int kS, bool kGated, int kMats, int kNT, bool kF16>
+template <int kS, bool kGated, int kMats, int kNT, bool kF16, bool kExact>
 __device__ __forceinline__ void gemm16_join(const Gemm16Args &a, const Gemm16Tile &ti, uint32_t part, int rank) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (ti.nvalid + kS - 1) / kS, c1 = min(ti.nvalid, (rank + 1) * per);
@@ -355,8 +355,8 @@ __device__ __forceinline__ void gemm16_join(const Gemm16Args &a, const Gemm16Til
       for (int k = 1; k < kS; ++k) t.x += v[k][m].x, t.y += v[k][m].y, t.z += v[k][m].z, t.w += v[k][m].w;
       p[m][0] = t.x, p[m][1] = t.y, p[m][2] = t.z, p[m][3] = t.w;
     }
-    gemm16_emit4<kGated, kF16>(a, ti.n0 + 4 * lane, ti.row0 + c, p[0], p[kMats - 1]);
-    if (kMats == 2 && !kGated) gemm16_emit4<false, kF16>(a, ti.n0 + 128 + 4 * lane, ti.row0 + c, p[1], p[1]);
+    gemm16_emit4<kGated, kF16, kExact>(a, ti.n0 + 4 * lane, ti.row0 + c, p[0], p[kMats - 1]);
+    if (kMats == 2 && !kGated) gemm16_emit4<false, kF16, kExact>(a, ti.n0 + 128 + 4 * lane, ti.row0 + c, p[1], p[1]);
   }
 }
 
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
           } else {
             uint16_t r[16] = {};
             if (a.residual) gemm16_residual(a, n, ti.row0 + c0, ti.nvalid - c0, r);
-            gemm16_emit<kGated, kF16, 16>(a, n, ti.row0 + c0, ti.nvalid - c0, b0, b1, r, sum[b][0], sum[b][kMats - 1]);
+            gemm16_emit<kGated, kF16, 16, true>(a, n, ti.row0 + c0, ti.nvalid - c0, b0, b1, r, sum[b][0], sum[b][kMats - 1]);
           }
         }
         continue;
@@ -642,9 +642,9 @@ __global__ void __launch_bounds__(kG16Threads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) part[(m * kNT + c0 + i) * 128 + q * 32 + lane] = p[m][i];
         } else {
-          gemm16_emit<kGated, kF16, 16, kGrouped>(a, n, ti.row0 + c0, ti.nvalid - c0, b0[0], b1[0], r[0], p[0], p[kMats - 1]);
+          gemm16_emit<kGated, kF16, 16, false, kGrouped>(a, n, ti.row0 + c0, ti.nvalid - c0, b0[0], b1[0], r[0], p[0], p[kMats - 1]);
           if (kSides == 2)
-            gemm16_emit<false, kF16, 16, kGrouped>(a, n + 128, ti.row0 + c0, ti.nvalid - c0, b0[kSides - 1], 0.f, r[kSides - 1], p[1],
+            gemm16_emit<false, kF16, 16, false, kGrouped>(a, n + 128, ti.row0 + c0, ti.nvalid - c0, b0[kSides - 1], 0.f, r[kSides - 1], p[1],
                                      p[1]);
 #pragma unroll
           for (int m = 0; m < kSides; ++m)
@@ -662,9 +662,9 @@ __global__ void __launch_bounds__(kG16Threads, 1)
     if (warp >= 2 && t0 < ntiles) {
       const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t0);
       const uint32_t part = smem_u32(smem);
-      if (S == 8) gemm16_join<8, kGated, kMats, kNT, kF16>(a, ti, part, rank);
-      else if (S == 4) gemm16_join<4, kGated, kMats, kNT, kF16>(a, ti, part, rank);
-      else gemm16_join<2, kGated, kMats, kNT, kF16>(a, ti, part, rank);
+      if (S == 8) gemm16_join<8, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
+      else if (S == 4) gemm16_join<4, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
+      else gemm16_join<2, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
     }
     cluster_sync_all();  // no CTA leaves while another may read its partials
   }

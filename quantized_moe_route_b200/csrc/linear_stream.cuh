@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kLsWarps * 32, 1)
       uint16_t r[1] = {0};
       gemm16_bias<kGated, kF16>(a.g, n0 + row, b0, b1);
       if (a.g.residual) gemm16_residual(a.g, n0 + row, t, 1, r);
-      gemm16_emit<kGated, kF16, 1>(a.g, n0 + row, t, 1, b0, b1, r, p0, p1);
+      gemm16_emit<kGated, kF16, 1, true>(a.g, n0 + row, t, 1, b0, b1, r, p0, p1);
     }
   }
   if (!ok)  // let the copies in flight land before the CTA leaves: stages cs, cs + 1, ... in order of issue

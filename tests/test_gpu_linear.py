@@ -425,3 +425,41 @@ def test_nan_passes_every_activation(T, N, K, out32, gated, act):
     hit[:, [1, N - 2, 7, N - 9]] = True
     assert torch.isnan(ys[1][hit]).all()
     assert torch.equal(ys[0][~hit], ys[1][~hit])
+
+
+@pytest.mark.parametrize("act,lo", [("silu", -60.0), ("sigmoid", -60.0), ("gelu", -9.0), ("gelu_tanh", -9.0)])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,N,K", [(16, 33, 1), (200, 40, 1), (100, 300, 2048), (2500, 2048, 64), (2500, 2048, 1024)])
+def test_activations_keep_their_relative_accuracy_in_the_tail(T, N, K, out, gated, act, lo):
+    """Arguments v below zero that arrive exactly (one input of x is v, its weight 1, all else 0; gated: up is 1).
+    In units of 2^-23 of the value: 16 for the functions and operations themselves (GELU's fit: 2^-20.3), the rounded
+    argument z of exp (v^2 / 2 within one half each of two roundings; 2 z' of tanh within 4), and for 16-bit results
+    __expf's documented 2 + 1.2 |z| and 4 for its division; then the result's rounding."""
+    dt = torch.float16 if out == "f16" else torch.bfloat16
+    rows = 2 * N if gated else N
+    v = torch.linspace(lo, -0.25, T, device="cuda").to(dt)
+    x = torch.zeros((T, up8(K)), dtype=dt, device="cuda")[:, :K]
+    x[:, K // 2] = v
+    w = torch.zeros((rows, up8(K)), dtype=dt, device="cuda")[:, :K]
+    w[:N, K // 2] = 1
+    b = torch.zeros(rows, dtype=dt, device="cuda")
+    b[N:] = 1
+    y = torch.empty((T, N), dtype=torch.float32 if out == "f32" else dt, device="cuda")
+    moe.moe_linear(x, w, y, bias=b, act=act_id(act), gated=gated)
+    v = v.double()
+    if act == "gelu_tanh":  # 1 + tanh cancels in 64 bits too: 1 / (1 + exp(-2 z))
+        z = 2 * (2 / torch.pi) ** 0.5 * (v + 0.044715 * v ** 3)
+        want, ulps = v * torch.special.expit(z), 16 + 4 * z.abs()
+    else:
+        z = -v * v / 2 if act == "gelu" else v
+        # (erfc, since ndtr is 0 in the tail)
+        want = v * 0.5 * torch.special.erfc(-v * 0.5 ** 0.5) if act == "gelu" else ACTS[act](v)
+        ulps = 16 + (z.abs() if act == "gelu" else 0)
+    if out != "f32":
+        ulps = ulps + 6 + 1.2 * z.abs()
+    tol = ulps * 2.0 ** -23 * want.abs()
+    if out != "f32":
+        tol = tol + torch.finfo(dt).eps / 2 * (want.abs() + tol) + (2.0 ** -25 if out == "f16" else 0)
+    err = (y.double() - want.unsqueeze(1)).abs()
+    assert (err <= tol.unsqueeze(1)).all(), f"worst {(err.max(1).values / tol).max().item():.2f} of the bound"
