@@ -27,6 +27,7 @@ MOE_W4_PLAIN, MOE_W4_GATE_UP = 0, 1
 MOE_BF16, MOE_F32, MOE_F16 = 0, 1, 2
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_SIGMOID = range(6)
 _TYPES = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_F16}
+_BF16, _F32, _I32 = (torch.bfloat16, torch.int16, torch.uint16), (torch.float32,), (torch.int32,)
 
 _lib = None
 _call = None      # the C helper's call(address, *args)
@@ -55,6 +56,7 @@ class moe_nvfp4_layer(ctypes.Structure):
 
 
 class moe_bf16_layer(ctypes.Structure):
+    device = None  # of the weights, where make_bf16_layer saw them
     _fields_ = [("E", ctypes.c_int), ("H", ctypes.c_int), ("F", ctypes.c_int),
                 ("gate_up", ctypes.c_void_p), ("down", ctypes.c_void_p)]
 
@@ -401,12 +403,20 @@ def _here(*tensors):
     return dev
 
 
-def _whole(*tensors):
-    """(tensor or None, bytes) pairs: each contiguous, of that many bytes, on the current CUDA device (returned)."""
+def _whole(layer, *tensors):
+    """(tensor or None, elements, types) triples: each of one of the types, contiguous, of that many elements, on
+    the current CUDA device (returned), where the layer's weights have to be too."""
     dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
-    for t, nbytes in tensors:
-        if t is not None and (t.get_device() != dev or t.nbytes != nbytes or not t.is_contiguous()):
-            _refuse("a tensor of another size, not contiguous, or not on the current CUDA device")
+    elsewhere = False
+    for t, n, types in tensors:
+        if t is not None:
+            if t.dtype not in types or t.numel() != n or not t.is_contiguous():
+                _refuse("a tensor of another type or size, or not contiguous")
+            elsewhere |= t.get_device() != dev
+    if elsewhere:
+        _refuse("tensors must be on the current CUDA device")
+    if layer.device not in (None, dev):
+        _refuse("the layer's weights are on another CUDA device")
     return dev
 
 
@@ -460,8 +470,18 @@ def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False,
 
 
 def make_bf16_layer(E, H, F, gate_up, down) -> moe_bf16_layer:
-    """Host descriptor of one layer's bf16 experts: gate_up [E][2F][H], down [E][H][F] (device buffers)."""
-    return moe_bf16_layer(E, H, F, gate_up.data_ptr(), down.data_ptr())
+    """Host descriptor of one layer's bf16 experts: gate_up [E][2F][H], down [E][H][F] (device buffers of bf16 or its
+    bits; buffers of more experts, or flat ones, will do)."""
+    for t, rows, cols in ((gate_up, 2 * F, H), (down, H, F)):
+        if t.dtype not in _BF16 or not t.is_contiguous():
+            _refuse("make_bf16_layer: weights of another type, or not contiguous")
+        if t.numel() < E * rows * cols or (t.dim() > 1 and t.shape[-1] != cols) or (t.dim() > 2 and t.shape[-2] != rows):
+            _refuse("make_bf16_layer: weights of another size")
+    if gate_up.get_device() < 0 or down.get_device() != gate_up.get_device():
+        _refuse("make_bf16_layer: weights must be on one CUDA device")
+    layer = moe_bf16_layer(E, H, F, gate_up.data_ptr(), down.data_ptr())
+    layer.device = gate_up.get_device()
+    return layer
 
 
 def moe_decode_layer_bf16_workspace_bytes(T, k, shared, E, H, F) -> int:
@@ -476,8 +496,9 @@ def moe_decode_layer_bf16(layer: moe_bf16_layer, x, k, y, ws, wr=None, logits=No
     Er = layer.E - shared
     if H != layer.H:
         _refuse("moe_decode_layer_bf16: x")
-    dev = _whole((x, 2 * T * H), (y, 2 * T * H), (wr, 2 * Er * H), (logits, 4 * T * Er), (shared_gate, 2 * H),
-                 (residual, 2 * T * H), (idx, 4 * T * k), (w, 4 * T * k), (ws, ws.nbytes))
+    n = T * H
+    dev = _whole(layer, (x, n, _BF16), (y, n, _BF16), (wr, Er * H, _BF16), (logits, T * Er, _F32), (shared_gate, H, _BF16),
+                 (residual, n, _BF16), (idx, T * k, _I32), (w, T * k, _F32), (ws, ws.numel(), (ws.dtype,)))
     _run("moe_decode_layer_bf16", ctypes.addressof(layer), x.data_ptr(), _ptr(wr), _ptr(logits), T, k, shared,
          _ptr(shared_gate), _ptr(residual), y.data_ptr(), _ptr(idx), _ptr(w), ws.data_ptr(), ws.nbytes, _on(stream, dev))
 
@@ -490,8 +511,8 @@ def moe_ffn_grouped_prefill_bf16(layer: moe_bf16_layer, x_perm, offsets, y_perm,
     rows, H = x_perm.shape
     if H != layer.H:
         _refuse("moe_ffn_grouped_prefill_bf16: x_perm")
-    dev = _whole((x_perm, 2 * rows * H), (y_perm, 2 * rows * H), (offsets, 4 * (layer.E + 1)),
-                 (ws, 0 if ws is None else ws.nbytes))
+    dev = _whole(layer, (x_perm, rows * H, _BF16), (y_perm, rows * H, _BF16), (offsets, layer.E + 1, _I32),
+                 (ws, 0 if ws is None else ws.numel(), () if ws is None else (ws.dtype,)))
     _run("moe_ffn_grouped_prefill_bf16", ctypes.addressof(layer), x_perm.data_ptr(), offsets.data_ptr(), rows,
          y_perm.data_ptr(), _ptr(ws), 0 if ws is None else ws.nbytes, _on(stream, dev))
 

@@ -538,3 +538,63 @@ def test_decode_one_infinite_feature(T, h, w):
     x[:, 1] = 1.0
     y, _, _, _ = run_decode(layer, x, 1, lg=torch.zeros((T, 4), device="cuda"))
     assert torch.equal(y, torch.full_like(y, math.copysign(math.inf, h * w)))
+
+
+def test_bindings_refuse_one_spoilt_tensor_of_a_valid_call():
+    """The valid call runs; with one tensor of another type of the same bytes, of another size, with gaps or on the CPU it
+    is refused, and nothing is written."""
+    layer = Layer16(210, 9, 128, 64)
+    gen = torch.Generator(device="cuda").manual_seed(211)
+    T, k = 2, 2
+    full = lambda shape, v, dt: torch.full(shape, v, dtype=dt, device="cuda")
+    dec = dict(x=normal(gen, (T, 128), 1.0), y=full((T, 128), 7.0, BF), wr=normal(gen, (8, 128), 0.1), logits=full((T, 8), 7.0, torch.float32),
+               shared_gate=normal(gen, (128,), 0.1), residual=normal(gen, (T, 128), 1.0),
+               idx=full((T, k), -7, torch.int32), w=full((T, k), 7.0, torch.float32))
+    ws = workspace(layer, T, k, 1)
+    grp = dict(x_perm=normal(gen, (4, 128), 1.0), offsets=torch.tensor([0, 1, 1, 1, 4, 4, 4, 4, 4, 4], dtype=torch.int32, device="cuda"),
+               y_perm=full((4, 128), 7.0, BF))
+    gws = torch.zeros(moe.moe_prefill_bf16_workspace_bytes(4, 64), dtype=torch.uint8, device="cuda")
+    calls = [(dec, ("y", "logits", "idx", "w"), lambda desc=layer.desc, **a: moe.moe_decode_layer_bf16(desc, k=k, ws=ws, shared=1, **a)),
+             (grp, ("y_perm",), lambda desc=layer.desc, **a: moe.moe_ffn_grouped_prefill_bf16(desc, ws=gws, **a))]
+    away = moe.make_bf16_layer(9, 128, 64, layer.gu, layer.dn)
+    away.device += 1
+    for args, outs, call in calls:
+        for name, t in args.items():
+            other = {BF: torch.float16, torch.float32: torch.int32, torch.int32: torch.float32}[t.dtype]
+            for bad in (t.view(other), t[..., 1:].contiguous(), torch.cat([t, t]), torch.stack([t, t], -1)[..., 0], t.cpu()):
+                with pytest.raises(moe.MoeError) as ei:
+                    call(**{**args, name: bad})
+                assert ei.value.status == moe.MOE_ERR_INVALID_ARG, name
+        with pytest.raises(moe.MoeError):
+            call(desc=away, **args)
+        torch.cuda.synchronize()
+        for o in outs:
+            assert (args[o].abs() == 7).all(), o
+        call(**args)
+        torch.cuda.synchronize()
+        for o in outs:
+            assert not (args[o].abs() == 7).all(), o
+    assert moe.moe_device_error() == 0
+
+
+@pytest.mark.parametrize("E, H, F", [(9, 128, 128), (9, 192, 64), (10, 128, 64)])
+def test_make_bf16_layer_refuses_weights_of_another_shape(E, H, F):
+    layer = Layer16(212, 9, 128, 64)
+    moe.make_bf16_layer(8, 128, 64, layer.gu, layer.dn)
+    with pytest.raises(moe.MoeError):
+        moe.make_bf16_layer(E, H, F, layer.gu, layer.dn)
+    for gu, dn in [(layer.gu.cpu(), layer.dn), (layer.gu, layer.dn.cpu()), (layer.gu.half(), layer.dn), (layer.gu, layer.dn.float())]:
+        with pytest.raises(moe.MoeError):
+            moe.make_bf16_layer(9, 128, 64, gu, dn)
+
+
+def test_bits_of_bf16_in_integer_tensors():
+    """int16 and uint16 tensors of bf16 bits, for any argument, give the same call."""
+    layer = Layer16(213, 4, 128, 64)
+    gen = torch.Generator(device="cuda").manual_seed(214)
+    x, lg = normal(gen, (3, 128), 1.0), torch.randn((3, 4), generator=gen, device="cuda")
+    want = run_decode(layer, x, 2, lg=lg)[0]
+    desc = moe.make_bf16_layer(4, 128, 64, layer.gu.view(torch.uint16), layer.dn.view(torch.int16))
+    y = torch.empty_like(want)
+    moe.moe_decode_layer_bf16(desc, x.view(torch.uint16), 2, y.view(torch.int16), workspace(layer, 3, 2, 0), logits=lg)
+    assert torch.equal(y, want)

@@ -136,3 +136,91 @@ def test_bf16_bindings_refuse_other_sizes_types_and_strides():
         with pytest.raises(moe.MoeError) as ei:
             moe.moe_decode_layer_bf16(layer, a.pop("x"), 2, a.pop("y"), torch.zeros(1 << 16, dtype=torch.uint8), **a)
         assert ei.value.status == INV, kw
+
+
+# CPU tensors are refused for their device, which is looked at last: the message tells which check refused a call
+def refusal(call, *args, **kw):
+    with pytest.raises(moe.MoeError) as ei:
+        call(*args, **kw)
+    assert ei.value.status == INV
+    return str(ei.value)
+
+
+def decode_args(**kw):
+    bf = torch.bfloat16
+    a = dict(layer=moe.moe_bf16_layer(9, 128, 64, P, P), x=torch.zeros(2, 128, dtype=bf), k=2,
+             y=torch.zeros(2, 128, dtype=bf), ws=torch.zeros(1 << 16, dtype=torch.uint8), wr=torch.zeros(8, 128, dtype=bf),
+             logits=torch.zeros(2, 8), shared=1, shared_gate=torch.zeros(128, dtype=bf),
+             residual=torch.zeros(2, 128, dtype=bf), idx=torch.zeros(2, 2, dtype=torch.int32), w=torch.zeros(2, 2))
+    a.update(kw)
+    return a
+
+
+# a tensor of the same bytes and another type, of another size, and with gaps, for each argument
+def spoilt(t):
+    other = {torch.bfloat16: torch.float16, torch.float32: torch.int32, torch.int32: torch.float32}[t.dtype]
+    return [t.view(other), t[..., 1:].contiguous(), torch.cat([t, t]), torch.stack([t, t], -1)[..., 0]]
+
+
+DECODE_TENSORS = ["x", "y", "wr", "logits", "shared_gate", "residual", "idx", "w"]
+
+
+def test_decode_binding_valid_call_is_refused_for_its_device_only():
+    assert "current CUDA device" in refusal(moe.moe_decode_layer_bf16, **decode_args())
+    bits = {n: decode_args()[n].view(v) for n, v in (("x", torch.int16), ("y", torch.uint16), ("wr", torch.int16))}
+    assert "current CUDA device" in refusal(moe.moe_decode_layer_bf16, **decode_args(**bits))
+
+
+@pytest.mark.parametrize("name", DECODE_TENSORS)
+@pytest.mark.parametrize("i", range(4))
+def test_decode_binding_refuses_each_tensor(name, i):
+    bad = spoilt(decode_args()[name])[i]
+    if name == "x" and i == 1:
+        assert "moe_decode_layer_bf16: x" in refusal(moe.moe_decode_layer_bf16, **decode_args(x=bad))
+    else:  # (more rows of x: y is then too short for them)
+        assert "another type or size" in refusal(moe.moe_decode_layer_bf16, **decode_args(**{name: bad}))
+
+
+def grouped_args(**kw):
+    bf = torch.bfloat16
+    a = dict(layer=moe.moe_bf16_layer(8, 128, 64, P, P), x_perm=torch.zeros(4, 128, dtype=bf),
+             offsets=torch.zeros(9, dtype=torch.int32), y_perm=torch.zeros(4, 128, dtype=bf),
+             ws=torch.zeros(4 * 64 * 2, dtype=torch.uint8))
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("name", ["x_perm", "offsets", "y_perm"])
+@pytest.mark.parametrize("i", range(4))
+def test_grouped_binding_refuses_each_tensor(name, i):
+    assert "current CUDA device" in refusal(moe.moe_ffn_grouped_prefill_bf16, **grouped_args())
+    msg = refusal(moe.moe_ffn_grouped_prefill_bf16, **grouped_args(**{name: spoilt(grouped_args()[name])[i]}))
+    assert ("grouped_prefill_bf16: x_perm" if name == "x_perm" and i == 1 else "another type or size") in msg
+
+
+def test_make_bf16_layer_refusals():
+    bf = torch.bfloat16
+    gu, dn = torch.zeros(4, 128, 192, dtype=bf), torch.zeros(4, 192, 64, dtype=bf)
+    ok = [(gu, dn), (gu.flatten(), dn.flatten()), (gu.view(torch.int16), dn.view(torch.uint16)),
+          (torch.cat([gu, gu]), torch.cat([dn, dn])), (gu.view(-1, 192), dn.view(-1, 64))]
+    for a, b in ok:
+        assert "one CUDA device" in refusal(moe.make_bf16_layer, 4, 192, 64, a, b)
+    for a, b in [(gu.half(), dn), (gu, dn.float()), (gu.transpose(1, 2), dn), (gu, dn[:, :, ::2])]:
+        assert "another type, or not contiguous" in refusal(moe.make_bf16_layer, 4, 192, 64, a, b)
+    for a, b in [(gu[:3], dn), (gu, dn[:3]), (gu.transpose(1, 2).contiguous(), dn), (gu, dn.transpose(1, 2).contiguous()),
+                 (gu.flatten()[1:], dn), (gu.view(2, 256, 192), dn)]:
+        assert "another size" in refusal(moe.make_bf16_layer, 4, 192, 64, a, b)
+
+
+@pytest.mark.parametrize("name", ["x", "w", "y", "bias", "residual"])
+@pytest.mark.parametrize("i", range(4))
+def test_linear_binding_refuses_each_tensor(name, i):
+    bf = torch.bfloat16
+    a = dict(x=torch.zeros(3, 16, dtype=bf), w=torch.zeros(8, 16, dtype=bf), y=torch.zeros(3, 8, dtype=bf),
+             bias=torch.zeros(8, dtype=bf), residual=torch.zeros(3, 8, dtype=bf))
+    assert "current CUDA device" in refusal(moe.moe_linear, **a)
+    bad = spoilt(a[name])[i]
+    if i == 3 and name != "bias":  # rows may lie apart, their elements may not
+        assert bad.stride(-1) == 2
+    a[name] = bad
+    assert "current CUDA device" not in refusal(moe.moe_linear, **a)
