@@ -26,7 +26,7 @@ MOE_DEVERR_DECODE_ROUTER_WAIT = 0x102
 MOE_W4_PLAIN, MOE_W4_GATE_UP = 0, 1
 MOE_BF16, MOE_F32, MOE_F16 = 0, 1, 2
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_SIGMOID = range(6)
-_TYPES = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.float16: MOE_F16}
+_TYPES = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.uint16: MOE_BF16, torch.float16: MOE_F16}
 _BF16, _F32, _I32 = (torch.bfloat16, torch.int16, torch.uint16), (torch.float32,), (torch.int32,)
 
 _lib = None
@@ -431,16 +431,15 @@ def _ptr(t):
 
 def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False, stream=None):
     """y [T][N] = act(x w^T + bias) + residual, or with gated (w [2N][K], gate rows first) act(g) * u + residual.
-    x [T][K], w, bias and residual are bf16 (or int16 bits) or f16; y is of the same type or fp32.  Tensors may
-    be rows of wider buffers (row strides of x and w in multiples of 8 elements)."""
+    x [T][K], w, bias and residual are bf16 (or its bits as int16 or uint16) or f16; y is of the same type or fp32.
+    Tensors may be rows of wider buffers (row strides of x and w in multiples of 8 elements)."""
     T, K = x.shape
     Ty, N = y.shape
     rows = 2 * N if gated else N
-    dtype, ydtype = x.dtype, y.dtype
-    dt = _TYPES.get(dtype, -1)
-    if w.shape != (rows, K) or Ty != T or w.dtype != dtype or dt < 0:
+    dt, ydtype = _TYPES.get(x.dtype, -1), y.dtype
+    if w.shape != (rows, K) or Ty != T or _TYPES.get(w.dtype) != dt:
         _refuse("moe_linear: shapes or types of x, w and y")
-    ydt = dt if ydtype == dtype else MOE_F32 if ydtype == torch.float32 else -1
+    ydt = MOE_F32 if ydtype == torch.float32 else dt if _TYPES.get(ydtype) == dt else -1
     # rows of contiguous elements; a single row has no next one, so any stride that the call accepts will do
     ldx, sx = x.stride()
     ldw, sw = w.stride()
@@ -454,12 +453,12 @@ def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False,
     bp = rp = None
     ldr = 0
     if bias is not None:
-        if bias.shape != (rows,) or bias.dtype != dtype or not bias.is_contiguous():
+        if bias.shape != (rows,) or _TYPES.get(bias.dtype) != dt or not bias.is_contiguous():
             _refuse("moe_linear: bias")
         bp = bias.data_ptr()
     if residual is not None:
         ldr, sr = residual.stride()
-        if residual.shape != (T, N) or residual.dtype != dtype or (sr != 1 and N > 1):
+        if residual.shape != (T, N) or _TYPES.get(residual.dtype) != dt or (sr != 1 and N > 1):
             _refuse("moe_linear: residual")
         if T <= 1:
             ldr = N

@@ -463,3 +463,23 @@ def test_activations_keep_their_relative_accuracy_in_the_tail(T, N, K, out, gate
         tol = tol + torch.finfo(dt).eps / 2 * (want.abs() + tol) + (2.0 ** -25 if out == "f16" else 0)
     err = (y.double() - want.unsqueeze(1)).abs()
     assert (err <= tol.unsqueeze(1)).all(), f"worst {(err.max(1).values / tol).max().item():.2f} of the bound"
+
+
+def test_bits_of_bf16_in_integer_tensors():
+    """bf16 tensors and int16 or uint16 tensors of bf16 bits, mixed, give the same call."""
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    bf = torch.bfloat16
+    x, w, b, r = ints(gen, (20, 72), bf), ints(gen, (24, 72), bf), ints(gen, (24,), bf), ints(gen, (20, 24), bf)
+    want, y = torch.empty((20, 24), dtype=bf, device="cuda"), torch.empty((20, 24), dtype=bf, device="cuda")
+    moe.moe_linear(x, w, want, bias=b, residual=r)
+    i16, u16 = torch.int16, torch.uint16
+    for dx, dw, db, dr, dy in [(i16,) * 5, (u16,) * 5, (u16, bf, i16, bf, u16), (bf, u16, u16, i16, bf)]:
+        y.zero_()
+        moe.moe_linear(x.view(dx), w.view(dw), y.view(dy), bias=b.view(db), residual=r.view(dr))
+        assert torch.equal(y, want), (dx, dw, db, dr, dy)
+    y32 = torch.empty((20, 24), device="cuda")
+    moe.moe_linear(x.view(u16), w, y32)
+    assert torch.equal(y32.double(), x.double() @ w.double().t())
+    for bad in (dict(x=x.view(torch.float16)), dict(w=w.view(torch.float16)), dict(y=y.view(torch.float16))):
+        with pytest.raises(moe.MoeError):
+            moe.moe_linear(**{**dict(x=x, w=w, y=y), **bad})
