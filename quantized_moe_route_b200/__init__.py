@@ -439,6 +439,8 @@ def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False,
     dt, ydtype = _TYPES.get(x.dtype, -1), y.dtype
     if w.shape != (rows, K) or Ty != T or _TYPES.get(w.dtype) != dt:
         _refuse("moe_linear: shapes or types of x, w and y")
+    if (T | rows | K) >> 31:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_linear")
     ydt = MOE_F32 if ydtype == torch.float32 else dt if _TYPES.get(ydtype) == dt else -1
     # rows of contiguous elements; a single row has no next one, so any stride that the call accepts will do
     ldx, sx = x.stride()

@@ -224,3 +224,14 @@ def test_linear_binding_refuses_each_tensor(name, i):
         assert bad.stride(-1) == 2
     a[name] = bad
     assert "current CUDA device" not in refusal(moe.moe_linear, **a)
+
+
+def test_linear_binding_refuses_sizes_past_32_bits():
+    """The ABI's sizes are ints: one that only 64 bits hold must not arrive as its lower half (2^32 rows as none)."""
+    bf = torch.bfloat16
+    wide = lambda r, c: torch.zeros(1, 1, dtype=bf).expand(r, c)
+    for n in (1 << 31, 1 << 32, (1 << 32) + 4):
+        for x, w, y in (((n, 8), (8, 8), (n, 8)), ((4, 8), (n, 8), (4, n)), ((4, n), (8, n), (4, 8))):
+            with pytest.raises(moe.MoeError) as ei:
+                moe.moe_linear(wide(*x), wide(*w), wide(*y))
+            assert ei.value.status == SHAPE, (x, w, y)
