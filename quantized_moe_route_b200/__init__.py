@@ -14,8 +14,6 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
@@ -26,10 +24,12 @@ MOE_DEVERR_DECODE_ROUTER_WAIT = 0x102
 MOE_W4_PLAIN, MOE_W4_GATE_UP = 0, 1
 MOE_BF16, MOE_F32, MOE_F16 = 0, 1, 2
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU, MOE_ACT_SIGMOID = range(6)
-_TYPES = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.uint16: MOE_BF16, torch.float16: MOE_F16}
-_BF16, _F32, _I32 = (torch.bfloat16, torch.int16, torch.uint16), (torch.float32,), (torch.int32,)
 
 _lib = None
+
+# of the 16-bit calls, set by the first of them
+torch = None
+_TYPES = _BF16 = _F32 = _I32 = None
 _call = None      # the C helper's call(address, *args)
 _address = {}     # entry points called through it
 
@@ -123,7 +123,7 @@ SIGNATURES = {
 
 def lib():
     """The loaded libmoe (raises if the in-tree build is missing)."""
-    global _lib, _call
+    global _lib
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"libmoe.so is not built ({LIB_PATH}); run quantized_moe_route_b200/build.py")
@@ -132,10 +132,6 @@ def lib():
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
-        from ._call import call
-        for name in ("moe_linear", "moe_decode_layer_bf16", "moe_ffn_grouped_prefill_bf16"):
-            _address[name] = ctypes.cast(getattr(L, name), ctypes.c_void_p).value
-        _call = call
         _lib = L
     return _lib
 
@@ -381,14 +377,32 @@ def moe_unpermute_combine(Y, w, y, inv=None, stream=None):
 
 
 # ---------------------------------------------------------------- 16-bit weights
+def _load_torch():
+    global torch, _TYPES, _BF16, _F32, _I32
+    import torch
+    _TYPES = {torch.bfloat16: MOE_BF16, torch.int16: MOE_BF16, torch.uint16: MOE_BF16, torch.float16: MOE_F16}
+    _BF16, _F32, _I32 = (torch.bfloat16, torch.int16, torch.uint16), (torch.float32,), (torch.int32,)
+
+
+def _load_call():
+    global _call
+    try:
+        from ._call import call
+    except ImportError as e:
+        raise ImportError("the 16-bit calls' helper _call.so is not built; run quantized_moe_route_b200/build.py") from e
+    for name in ("moe_linear", "moe_decode_layer_bf16", "moe_ffn_grouped_prefill_bf16"):
+        _address[name] = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+    _call = call
+
+
 def _refuse(why):
     raise MoeError(MOE_ERR_INVALID_ARG, why)
 
 
 def _run(name, *args):
     """Enqueues an entry point whose arguments are integers, addresses or None."""
-    if _lib is None:
-        lib()
+    if _call is None:
+        _load_call()
     status = _call(_address[name], *args)
     if status != MOE_OK:
         raise MoeError(status, name)
@@ -433,6 +447,8 @@ def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False,
     """y [T][N] = act(x w^T + bias) + residual, or with gated (w [2N][K], gate rows first) act(g) * u + residual.
     x [T][K], w, bias and residual are bf16 (or its bits as int16 or uint16) or f16; y is of the same type or fp32.
     Tensors may be rows of wider buffers (row strides of x and w in multiples of 8 elements)."""
+    if torch is None:
+        _load_torch()
     T, K = x.shape
     Ty, N = y.shape
     rows = 2 * N if gated else N
@@ -473,6 +489,8 @@ def moe_linear(x, w, y, bias=None, residual=None, act=MOE_ACT_NONE, gated=False,
 def make_bf16_layer(E, H, F, gate_up, down) -> moe_bf16_layer:
     """Host descriptor of one layer's bf16 experts: gate_up [E][2F][H], down [E][H][F] (device buffers of bf16 or its
     bits; buffers of more experts, or flat ones, will do)."""
+    if torch is None:
+        _load_torch()
     for t, rows, cols in ((gate_up, 2 * F, H), (down, H, F)):
         if t.dtype not in _BF16 or not t.is_contiguous():
             _refuse("make_bf16_layer: weights of another type, or not contiguous")
@@ -493,6 +511,8 @@ def moe_decode_layer_bf16(layer: moe_bf16_layer, x, k, y, ws, wr=None, logits=No
                           residual=None, idx=None, w=None, stream=None):
     """One layer with bf16 experts: the router (from wr, or logits as given), routing, expert FFN, the optional
     shared expert (with its sigmoid gate), combine, residual."""
+    if torch is None:
+        _load_torch()
     T, H = x.shape
     Er = layer.E - shared
     if H != layer.H:
@@ -509,6 +529,8 @@ def moe_prefill_bf16_workspace_bytes(rows, F) -> int:
 
 
 def moe_ffn_grouped_prefill_bf16(layer: moe_bf16_layer, x_perm, offsets, y_perm, ws, stream=None):
+    if torch is None:
+        _load_torch()
     rows, H = x_perm.shape
     if H != layer.H:
         _refuse("moe_ffn_grouped_prefill_bf16: x_perm")

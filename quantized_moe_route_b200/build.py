@@ -47,9 +47,13 @@ def build_call(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    build_call(force)
-    if not force and not needs_build():
-        return LIB
+    if force or needs_build():
+        build_lib(verbose)
+    build_call(force)  # last: the library serves every other call without it
+    return LIB
+
+
+def build_lib(verbose: bool = False) -> None:
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]
@@ -58,7 +62,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
