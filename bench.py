@@ -1288,6 +1288,16 @@ def run_reference(args, log):
 
 
 # ---------------------------------------------------------------------------- main
+def result_lines(out):
+    """(the JSON line, lines for stderr): the legs' whole records are some 25 KB, too long for a reader of the
+    line that keeps the end of the output, so the line holds their figures and stderr their records."""
+    legs = out.get("legs", {})
+    sig = lambda v: float(f"{v:.5g}") if v is not None else None
+    brief = {n: {"value": sig(v["value"]), "unit": v["unit"], "e2e": sig(v["e2e"]["value"]), "frac": sig(v["roofline"]["frac"])}
+             for n, v in legs.items()}
+    return json.dumps({**out, "legs": brief} if legs else out), [f"[bench] leg {n}: {json.dumps(v)}" for n, v in legs.items()]
+
+
 def run_native(args, log):
     ctx = Ctx(args, log)
     wl = args.workload
@@ -1391,7 +1401,10 @@ def main():
     else:
         out = run_native(args, log)
     if out is not None:
-        print(json.dumps(out), flush=True)
+        line, records = result_lines(out)
+        for r in records:
+            print(r, file=sys.stderr, flush=True)
+        print(line, flush=True)
 
 
 if __name__ == "__main__":

@@ -48,3 +48,26 @@ def test_throughput_and_peaks():
     assert peak > 1000 and kind in ("measured", "fallback")
     alu, akind = bench.alu_peak()
     assert abs(alu - 148 * 128 * 1965e6 / 1e12) < 1.0 and akind.startswith("derived")
+
+
+def test_result_line_stays_short_with_every_leg():
+    """The line carries the contract's keys unchanged and each leg's figures in under 3600 characters; the legs' records
+    go to stderr whole."""
+    leg = {"metric": bench.METRIC, "value": 45577.18839066676, "unit": "tokens/s", "n_gpus": 1, "steps": 20, "warmup": 5,
+           "ms_per_step": 0.021940800000000003, "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+           "dtype": bench.DTYPE_W4, "data": "synthetic", "config": {"workload": "w" * 500},
+           "roofline": {"bound": "hbm", "frac": 0.17330865452654687, "how": "r" * 400},
+           "e2e": {"value": 13165697019.755371, "unit": "tokens/s", "h2d_bytes_per_step": 134217728, "d2h_bytes_per_step": 33},
+           "gpu_launches": 20, "clocks": {"sm_mhz": 1965.0, "sm_max_mhz": 1965.0, "reasons": [], "samples": 3},
+           "cpu_baseline": {"value": 2.35, "unit": "tokens/s", "cores": 16, "kind": "oracle", "sample": "s" * 250}}
+    names = [f"decode_stream_T{i}" for i in range(12)]
+    out = {**leg, "legs": {n: dict(leg) for n in names}, "gpu_launches_all_legs": 260}
+    line, records = bench.result_lines(out)
+    assert len(line) < 3600 and "\n" not in line
+    d = json.loads(line)
+    for k in leg:
+        assert d[k] == leg[k], k
+    assert list(d["legs"]) == names and d["gpu_launches_all_legs"] == 260
+    assert d["legs"][names[0]] == {"value": 45577.0, "unit": "tokens/s", "e2e": 13166000000.0, "frac": 0.17331}
+    assert [json.loads(r.split(": ", 1)[1]) for r in records] == [leg] * 12
+    assert bench.result_lines(leg) == (json.dumps(leg), [])
