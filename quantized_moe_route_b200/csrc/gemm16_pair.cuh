@@ -151,6 +151,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kG16Threads, 1)
           if (++s == C::kStages) s = 0, ph ^= 1u;
         }
       }
+      // The leader's products also arrive on the other CTA's `empty` barriers: a
+      // CTA stays until the last arrival of each stage has come.
+      for (int i = 0; i < C::kStages && ok && !*abort_s; ++i) {
+        if (!mbar_wait_cluster(&empty[s], ph ^ 1u, kG16WaitPolls)) {
+          fail();
+          ok = false;
+        }
+        if (++s == C::kStages) s = 0, ph ^= 1u;
+      }
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {

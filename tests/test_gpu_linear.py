@@ -483,3 +483,23 @@ def test_bits_of_bf16_in_integer_tensors():
     for bad in (dict(x=x.view(torch.float16)), dict(w=w.view(torch.float16)), dict(y=y.view(torch.float16))):
         with pytest.raises(moe.MoeError):
             moe.moe_linear(**{**dict(x=x, w=w, y=y), **bad})
+
+
+def test_pairs_of_sms_back_to_back_with_other_kernels():
+    """The kernel on pairs of SMs in turn with the tiles and the weight stream, launches following one another closely:
+    no CTA's late arrivals reach a successor (the same bits as alone)."""
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    w = torch.randn((2048, 1024), generator=gen, device="cuda").bfloat16()
+    xs = [torch.randn((T, 1024), generator=gen, device="cuda").bfloat16() for T in (2500, 2500, 300, 40, 9)]
+    ys = [torch.empty((x.shape[0], 2048), dtype=torch.bfloat16, device="cuda") for x in xs]
+    for x, y in zip(xs, ys):
+        moe.moe_linear(x, w, y)
+        torch.cuda.synchronize()
+    alone = [y.clone() for y in ys]
+    for y in ys:
+        y.zero_()
+    for _ in range(200):
+        for x, y in zip(xs, ys):
+            moe.moe_linear(x, w, y)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, y) for a, y in zip(alone, ys)) and moe.moe_device_error() == 0
