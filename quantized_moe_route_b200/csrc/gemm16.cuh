@@ -266,7 +266,7 @@ __device__ __forceinline__ float gemm16_half(uint32_t v, int hi) {
 }
 
 // Sixteen consecutive outputs n .. n + 15 (those below a.N) of row `row`, from
-// their products and the row's residual: as gemm16_emit.  kBare: the grouped
+// their products and the row's residual: as gemm16_emit, y 16-bit.  kBare: the grouped
 // FFN's, SiLU on the gate or nothing, bf16 outputs in whole vectors (a kernel's
 // first pass over its code is a walk through the instruction cache: with the
 // linear's epilogue in its place a small prompt takes 3 us more).
@@ -304,32 +304,19 @@ __device__ __forceinline__ void gemm16_emit_row(const Gemm16Args &a, int n, int6
 #pragma unroll
     for (int i = 0; i < 16; ++i) p0[i] += gemm16_half<kF16>(r[i >> 1], i & 1);
   }
-  if (a.y_f32) {
-    float *y = static_cast<float *>(a.y) + row * a.ldy + n;
-    if (nv >= 16 && reinterpret_cast<uintptr_t>(y) % 16 == 0) {
+  uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.ldy + n;
+  uint32_t o[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4 *>(y)[i] = make_float4(p0[4 * i], p0[4 * i + 1], p0[4 * i + 2], p0[4 * i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < nv) y[i] = p0[i];
-    }
+  for (int i = 0; i < 8; ++i)
+    o[i] = kF16 ? (uint32_t)f32_to_w16<true>(p0[2 * i]) | (uint32_t)f32_to_w16<true>(p0[2 * i + 1]) << 16
+                : cvt_bf16x2(p0[2 * i], p0[2 * i + 1]);
+  if (nv >= 16 && reinterpret_cast<uintptr_t>(y) % 16 == 0) {
+    reinterpret_cast<uint4 *>(y)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4 *>(y)[1] = make_uint4(o[4], o[5], o[6], o[7]);
   } else {
-    uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.ldy + n;
-    uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      o[i] = kF16 ? (uint32_t)f32_to_w16<true>(p0[2 * i]) | (uint32_t)f32_to_w16<true>(p0[2 * i + 1]) << 16
-                  : cvt_bf16x2(p0[2 * i], p0[2 * i + 1]);
-    if (nv >= 16 && reinterpret_cast<uintptr_t>(y) % 16 == 0) {
-      reinterpret_cast<uint4 *>(y)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<uint4 *>(y)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < nv) y[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
-    }
+    for (int i = 0; i < 16; ++i)
+      if (i < nv) y[i] = (uint16_t)(o[i >> 1] >> (16 * (i & 1)));
   }
 }
 
@@ -338,6 +325,7 @@ __device__ __forceinline__ void gemm16_emit_row(const Gemm16Args &a, int n, int6
 // four of its 128 outputs, with the loads from all CTAs in flight together.
 template <int kS, bool kGated, int kMats, int kNT, bool kF16, bool kExact>
 __device__ __forceinline__ void gemm16_join(const Gemm16Args &a, const Gemm16Tile &ti, uint32_t part, int rank) {
+  static_assert(kMats == 1 || kGated, "128 outputs a tile");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (ti.nvalid + kS - 1) / kS, c1 = min(ti.nvalid, (rank + 1) * per);
   part += (uint32_t)lane * 16u;
@@ -356,7 +344,6 @@ __device__ __forceinline__ void gemm16_join(const Gemm16Args &a, const Gemm16Til
       p[m][0] = t.x, p[m][1] = t.y, p[m][2] = t.z, p[m][3] = t.w;
     }
     gemm16_emit4<kGated, kF16, kExact>(a, ti.n0 + 4 * lane, ti.row0 + c, p[0], p[kMats - 1]);
-    if (kMats == 2 && !kGated) gemm16_emit4<false, kF16, kExact>(a, ti.n0 + 128 + 4 * lane, ti.row0 + c, p[1], p[1]);
   }
 }
 
@@ -367,7 +354,10 @@ __global__ void __launch_bounds__(kG16Threads, 1)
   using C = Gemm16Cfg<kMats, kNT>;
   static_assert(!kGated || kMats == 2, "gate and up");
   constexpr bool kCanFlip = kMats == 2 && kNT == 128;  // rows on M, two weight blocks on N
+  constexpr bool kOnlyFlip = kCanFlip && !kGrouped && !kGated;  // the dense linear's two blocks of outputs: flip = 0
+  constexpr bool kSplits = !kGrouped && !kOnlyFlip;             // K may be shared by a cluster
   constexpr int kOut = kGated ? 128 : 128 * kMats;  // outputs per tile
+  auto flipped = [&](const Gemm16Tile &ti) { return kCanFlip && (kOnlyFlip || ti.nvalid > a.flip); };
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);  // (keeps the address space known)
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kTailOff);
@@ -425,7 +415,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
   const uint32_t tmem = *tmem_base_s;
   const int nchunks = kGrouped ? start[a.E] : (a.rows + a.nt - 1) / a.nt;
   const int ntiles = nchunks * a.nfb;
-  const int S = kGrouped ? 1 : a.splits, rank = S > 1 ? (int)cluster_rank() : 0;
+  const int S = kSplits ? a.splits : 1, rank = S > 1 ? (int)cluster_rank() : 0;
   const int t0 = blockIdx.x / S, G = gridDim.x / S;
   const int KB = (a.K + kG16BK - 1) / kG16BK;
   const int kb0 = KB * rank / S, kb1 = KB * (rank + 1) / S;  // S <= KB: never empty
@@ -473,7 +463,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
       uint32_t ph = 0, tc = 0;
       for (int t = t0; t < ntiles && !*abort_s; t += G) {
         const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t);
-        const uint32_t idesc = idesc_16_f32(kCanFlip && ti.nvalid > a.flip ? 256 : (ti.nvalid + 15) & ~15, kF16);
+        const uint32_t idesc = idesc_16_f32(flipped(ti) ? 256 : (ti.nvalid + 15) & ~15, kF16);
         bool ok = true;
         for (int kb = kb0; kb < kb1 && ok; ++tc) {  // accumulations: one, or one a segment
           const uint32_t acc = tmem + (tc & 1u) * C::kAccCols;
@@ -492,7 +482,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
             }
             tc_fence_after();
             const uint64_t ad = desc0 + ((uint32_t)s * stage >> 4), bd = ad + (C::kABytes >> 4);
-            if (kCanFlip && ti.nvalid > a.flip) {
+            if (flipped(ti)) {
 #pragma unroll
               for (int kk = 0; kk < kG16BK / 16; ++kk)
                 tc_mma_bf16(acc, bd + (kk * 32 >> 4), ad + (kk * 32 >> 4), idesc, (kb > first || kk) ? 1u : 0u);
@@ -575,15 +565,11 @@ __global__ void __launch_bounds__(kG16Threads, 1)
         }
         continue;
       }
-      constexpr int kSides = kMats == 2 && !kGated ? 2 : 1;  // outputs n and n + 128
-      float b0[kSides] = {}, b1[kSides] = {};
-      uint16_t r[kSides][16] = {};
-      if (!kGrouped && S == 1 && !(kCanFlip && ti.nvalid > a.flip)) {  // what does not depend on the products, before waiting for them
-#pragma unroll
-        for (int m = 0; m < kSides; ++m) {
-          gemm16_bias<kGated, kF16>(a, n + 128 * m, b0[m], b1[m]);
-          if (a.residual) gemm16_residual(a, n + 128 * m, ti.row0 + sub * 16, ti.nvalid - sub * 16, r[m]);
-        }
+      float b0 = 0.f, b1 = 0.f;
+      uint16_t r[16] = {};
+      if (!kGrouped && S == 1 && !flipped(ti)) {  // what does not depend on the products, before waiting for them
+        gemm16_bias<kGated, kF16>(a, n, b0, b1);
+        if (a.residual) gemm16_residual(a, n, ti.row0 + sub * 16, ti.nvalid - sub * 16, r);
       }
       if (!mbar_wait_sleep(&acc_full[tc & 1u], (tc >> 1) & 1u, kG16WaitPolls)) {
         fail();
@@ -591,7 +577,7 @@ __global__ void __launch_bounds__(kG16Threads, 1)
       }
       tc_fence_after();
       const uint32_t acc = tmem + (tc & 1u) * C::kAccCols + ((uint32_t)(q * 32) << 16);
-      if (kCanFlip && ti.nvalid > a.flip) {
+      if (flipped(ti)) {
         // lane: row 32 q + lane; columns: the tile's outputs (gated: gate, then up)
         const int row = q * 32 + lane, outs = min(kOut, a.N - ti.n0);
         const bool live = row < ti.nvalid;
@@ -616,57 +602,54 @@ __global__ void __launch_bounds__(kG16Threads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) rr[i] = rnext[i];
           }
-      } else
-      for (int c0 = sub * 16; c0 < ti.nvalid; c0 += kStep) {
-        uint32_t v[kMats][16];
+      } else if constexpr (!kOnlyFlip) {
+        for (int c0 = sub * 16; c0 < ti.nvalid; c0 += kStep) {
+          uint32_t v[kMats][16];
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) tmem_ld16_async(acc + m * kNT + c0, v[m]);
-        uint16_t rn[kSides][16] = {};
-        if (!kGrouped && a.residual && S == 1) {  // the next batch's
+          for (int m = 0; m < kMats; ++m) tmem_ld16_async(acc + m * kNT + c0, v[m]);
+          uint16_t rn[16] = {};
+          if (!kGrouped && a.residual && S == 1)  // the next batch's
+            gemm16_residual(a, n, ti.row0 + c0 + kStep, ti.nvalid - c0 - kStep, rn);
+          tmem_ld_wait();
+          float p[2][16];
 #pragma unroll
-          for (int m = 0; m < kSides; ++m)
-            gemm16_residual(a, n + 128 * m, ti.row0 + c0 + kStep, ti.nvalid - c0 - kStep, rn[m]);
-        }
-        tmem_ld_wait();
-        float p[2][16];
+          for (int m = 0; m < kMats; ++m) {
+            tmem_regs_after_wait(v[m]);
 #pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-          tmem_regs_after_wait(v[m]);
+            for (int i = 0; i < 16; ++i) p[m][i] = __uint_as_float(v[m][i]);
+          }
+          if (S > 1) {  // partials: [block][row][128 outputs]
+            float *part = reinterpret_cast<float *>(smem);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[m][i] = __uint_as_float(v[m][i]);
-        }
-        if (S > 1) {  // partials: [block][row][128 outputs]
-          float *part = reinterpret_cast<float *>(smem);
+            for (int m = 0; m < kMats; ++m)
 #pragma unroll
-          for (int m = 0; m < kMats; ++m)
+              for (int i = 0; i < 16; ++i) part[(m * kNT + c0 + i) * 128 + q * 32 + lane] = p[m][i];
+          } else {
+            gemm16_emit<kGated, kF16, 16, false, kGrouped>(a, n, ti.row0 + c0, ti.nvalid - c0, b0, b1, r, p[0], p[kMats - 1]);
+            if (kMats == 2 && !kGated)  // grouped: outputs n and n + 128
+              gemm16_emit<false, kF16, 16, false, true>(a, n + 128, ti.row0 + c0, ti.nvalid - c0, 0.f, 0.f, r, p[1], p[1]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[(m * kNT + c0 + i) * 128 + q * 32 + lane] = p[m][i];
-        } else {
-          gemm16_emit<kGated, kF16, 16, false, kGrouped>(a, n, ti.row0 + c0, ti.nvalid - c0, b0[0], b1[0], r[0], p[0], p[kMats - 1]);
-          if (kSides == 2)
-            gemm16_emit<false, kF16, 16, false, kGrouped>(a, n + 128, ti.row0 + c0, ti.nvalid - c0, b0[kSides - 1], 0.f, r[kSides - 1], p[1],
-                                     p[1]);
-#pragma unroll
-          for (int m = 0; m < kSides; ++m)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) r[m][i] = rn[m][i];
+            for (int i = 0; i < 16; ++i) r[i] = rn[i];
+          }
         }
       }
       tc_fence_before();
       mbar_arrive(&acc_empty[tc & 1u]);
     }
   }
-  if (S > 1) {  // one tile per cluster; every thread of every CTA comes here, aborted or not
-    __syncwarp();
-    cluster_sync_all();
-    if (warp >= 2 && t0 < ntiles) {
-      const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t0);
-      const uint32_t part = smem_u32(smem);
-      if (S == 8) gemm16_join<8, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
-      else if (S == 4) gemm16_join<4, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
-      else gemm16_join<2, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
+  if constexpr (kSplits) {
+    if (S > 1) {  // one tile per cluster; every thread of every CTA comes here, aborted or not
+      __syncwarp();
+      cluster_sync_all();
+      if (warp >= 2 && t0 < ntiles) {
+        const Gemm16Tile ti = gemm16_tile<kGrouped, kOut>(a, start, t0);
+        const uint32_t part = smem_u32(smem);
+        if (S == 8) gemm16_join<8, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
+        else if (S == 4) gemm16_join<4, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
+        else gemm16_join<2, kGated, kMats, kNT, kF16, kSeg>(a, ti, part, rank);
+      }
+      cluster_sync_all();  // no CTA leaves while another may read its partials
     }
-    cluster_sync_all();  // no CTA leaves while another may read its partials
   }
   tc_fence_before();
   __syncthreads();
