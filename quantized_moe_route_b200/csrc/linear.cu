@@ -71,12 +71,12 @@ static void gemm16_plan(Gemm16Args &a, const DeviceInfo &d) {
   }
 }
 
-template <bool kGated, bool kF16, bool kF32Out>
+template <bool kGated, bool kF16, bool kSegments>
 static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const void *w, int64_t ldw, const DeviceInfo &d,
                               cudaStream_t s) {
   // gated: gate and up of 128 features and 128 rows a tile; else 128 outputs and 256 rows
-  // (fp32 outputs are summed in segments that the epilogue's registers hold: three quarters of the rows)
-  constexpr int kMats = kGated ? 2 : 1, kNT = (kF32Out ? 192 : 256) / kMats;
+  // (in segments the sums stand in the epilogue's registers: three quarters of the rows)
+  constexpr int kMats = kGated ? 2 : 1, kNT = (kSegments ? 192 : 256) / kMats;
   CUtensorMap wm, x64, x16;
   if (!gemm16_map(&wm, w, (int64_t)a.N * (kGated ? 2 : 1), a.K, ldw, 128, kF16) ||
       !gemm16_map(&x64, x, a.rows, a.K, ldx, 64, kF16) || !gemm16_map(&x16, x, a.rows, a.K, ldx, 16, kF16)) {
@@ -96,7 +96,7 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
                        (!a.residual || (a.ldr % 8 == 0 && reinterpret_cast<uintptr_t>(a.residual) % 16 == 0));
   const int nfb = (a.N + (kGated ? 127 : 255)) / (kGated ? 128 : 256);
   const int64_t tiles1 = (int64_t)nfb * ((a.rows + 127) / 128), tiles2 = (int64_t)nfb * ((a.rows + 255) / 256);
-  if (!kF32Out && vectors && tiles1 >= (kGated ? d.sms / 2 : 3 * d.sms / 4)) {
+  if (!kSegments && vectors && tiles1 >= (kGated ? d.sms / 2 : 3 * d.sms / 4)) {
     a.mat_off = kGated ? a.N : 128;
     a.nfb = nfb;
     a.nt = 128;
@@ -114,14 +114,14 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
   a.mat_off = a.N;
   a.nfb = (a.N + 127) / 128;
   a.flip = 128;
-  gemm16_plan<kGated, kMats, kNT, kF16, kF32Out>(a, d);
+  gemm16_plan<kGated, kMats, kNT, kF16, kSegments>(a, d);
   const int64_t tiles = (int64_t)a.nfb * ((a.rows + a.nt - 1) / a.nt);
   const int grid = a.splits > 1 ? (int)tiles * a.splits : (int)(tiles < d.sms ? tiles : d.sms);
-  if constexpr (kF32Out) {  // the sums of up to two thirds of the rows fit in registers with the rest (5 % faster there)
+  if constexpr (kSegments) {  // up to two thirds of the rows: fewer sums in registers (5 % faster there; only the gated kernel spills, 28 bytes)
     constexpr int kFew = 128 / kMats;
     if (a.nt <= kFew) return gemm16_launch<false, kGated, kMats, kFew, kF16, true>(a, grid, wm, x64, x16, d.dev, s);
   }
-  return gemm16_launch<false, kGated, kMats, kNT, kF16, kF32Out>(a, grid, wm, x64, x16, d.dev, s);
+  return gemm16_launch<false, kGated, kMats, kNT, kF16, kSegments>(a, grid, wm, x64, x16, d.dev, s);
 }
 
 }  // namespace moe
@@ -163,10 +163,14 @@ extern "C" MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void 
   cudaStream_t s = as_stream(stream);
   DeviceInfo d;
   if (!device_info(&d)) return MOE_ERR_CUDA;
+  // Sums in segments where the tensor core's truncating additions would show:
+  // they leave a sum 6e-9 K too small (K = 32768: 1.9e-4, two fifths of half a
+  // step of f16; K = 2^18: 1.6e-3, two fifths of half a step of bf16).
+  const bool segments = a.y_f32 || K > (dtype == MOE_F16 ? 1 << 15 : 1 << 18);
   const bool f16 = dtype == MOE_F16, stream_w = linear_streams(T, N, K, gated, d.sms);
 #define MOE_LINEAR(GATED, F16)                                                        \
   (stream_w    ? linear_stream<GATED, F16>(a, x, ldx, w, ldw, d, s)                   \
-   : a.y_f32   ? linear_gemm<GATED, F16, true>(a, x, ldx, w, ldw, d, s)               \
+   : segments  ? linear_gemm<GATED, F16, true>(a, x, ldx, w, ldw, d, s)               \
                : linear_gemm<GATED, F16, false>(a, x, ldx, w, ldw, d, s))
   if (f16) return gated ? MOE_LINEAR(true, true) : MOE_LINEAR(false, true);
   return gated ? MOE_LINEAR(true, false) : MOE_LINEAR(false, false);

@@ -22,6 +22,10 @@ namespace moe {
 
 constexpr int kLsWarps = 8;
 constexpr int kLsCols = 2;    // 64-input columns of a stage
+// Pairs of columns of a warp between additions of its accumulators to its sums:
+// the tensor core's fp32 additions truncate, by up to a unit in the last place
+// each (K = 2^20 without: 1.7e-4 too small), so an accumulation has at most 16.
+constexpr int kLsFold = 8;
 constexpr uint32_t kLsPolls = 1u << 20;
 
 struct LinearStreamArgs {
@@ -128,8 +132,19 @@ __global__ void __launch_bounds__(kLsWarps * 32, 1)
   uint32_t parity = 0;
   bool ok = true;
   for (int s = 0; s < nstrips; ++s) {
-    float acc[NB][4][4] = {};
+    float acc[NB][4][4] = {}, sum[NB][4] = {};
+    auto fold = [&]() {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[nb][i] += (acc[nb][0][i] + acc[nb][1][i]) + (acc[nb][2][i] + acc[nb][3][i]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[nb][j][i] = 0.f;
+        }
+    };
     for (int c = 0; c < cols && ok; ++c) {
+      if (c && c % kLsFold == 0) fold();
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[cs], parity, kLsPolls))) {
         if (lane == 0) atomicExch(a.g.err, DEVERR_PREFILL_WAIT);
         ok = false;
@@ -153,17 +168,15 @@ __global__ void __launch_bounds__(kLsWarps * 32, 1)
       issue();
       if (++cs == C::kStages) cs = 0, parity ^= 1u;
     }
+    fold();
     // partial sums [row][token], two buffers in turn: one barrier a strip
     float *part = reinterpret_cast<float *>(smem + C::kPartOff + (s & 1) * (kLsWarps * C::kPart));
     float *mine = part + warp * (C::kPart / 4);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (acc[nb][0][i] + acc[nb][1][i]) + (acc[nb][2][i] + acc[nb][3][i]);
       const int n = nb * 8 + 2 * t4;
-      *reinterpret_cast<float2 *>(mine + g * 8 * NB + n) = make_float2(v[0], v[1]);
-      *reinterpret_cast<float2 *>(mine + (g + 8) * 8 * NB + n) = make_float2(v[2], v[3]);
+      *reinterpret_cast<float2 *>(mine + g * 8 * NB + n) = make_float2(sum[nb][0], sum[nb][1]);
+      *reinterpret_cast<float2 *>(mine + (g + 8) * 8 * NB + n) = make_float2(sum[nb][2], sum[nb][3]);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * gs) : "memory");
     const int n0 = (first + s * step) * per;

@@ -503,3 +503,28 @@ def test_pairs_of_sms_back_to_back_with_other_kernels():
             moe.moe_linear(x, w, y)
     torch.cuda.synchronize()
     assert all(torch.equal(a, y) for a, y in zip(alone, ys)) and moe.moe_device_error() == 0
+
+
+@pytest.mark.parametrize("T,N,K,dtype,out32", [
+    (1, 24, 16384, "bf16", True), (5, 24, 65536, "bf16", True), (16, 24, 1 << 20, "f16", True), (30, 24, 65536, "f16", True),
+    (40, 24, 1 << 17, "bf16", True), (3, 24, 1 << 20, "f16", False), (40, 24, 1 << 18, "f16", False),
+    (2500, 2048, 1 << 16, "f16", False), (40, 24, 1 << 20, "bf16", False)])
+def test_long_sums_of_one_sign(T, N, K, dtype, out32):
+    """Products of one sign, the worst case of additions that truncate: a segment of at most 512 inputs a chain takes at
+    most 32 of them, 33 2^-23 with the products' own, and the additions of segments, rounded to nearest, at most 2^-24
+    each.  Their directions are random, so the error as a whole stays at 2^-19; a 16-bit result has its rounding too."""
+    gen = torch.Generator(device="cuda").manual_seed(T + K)
+    dt = DT[dtype]
+    x = torch.rand((T, K), generator=gen, device="cuda").to(dt)
+    w = (torch.rand((N, K), generator=gen, device="cuda") * (4 / K if dtype == "bf16" else 1 / 256)).to(dt)
+    y = torch.empty((T, N), dtype=torch.float32 if out32 else dt, device="cuda")
+    moe.moe_linear(x, w, y)
+    want = torch.zeros((T, N), dtype=torch.float64, device="cuda")
+    for k in range(0, K, 1 << 14):
+        want += x[:, k:k + (1 << 14)].double() @ w[:, k:k + (1 << 14)].double().t()
+    rel = (y.double() - want) / want
+    tol = 33 * 2.0 ** -23 + K / 512 * 2.0 ** -24
+    if out32:
+        assert rel.abs().max() <= tol and rel.norm() / rel.numel() ** 0.5 <= 2.0 ** -19
+    else:
+        assert rel.abs().max() <= torch.finfo(dt).eps / 2 + 2 * tol
