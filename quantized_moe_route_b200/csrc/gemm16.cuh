@@ -35,7 +35,7 @@ namespace moe {
 constexpr int kG16BK = 64;
 constexpr uint32_t kG16Ring = 216 * 1024;  // bytes of the stage ring: 4 stages of the largest tiles, more of smaller ones
 constexpr int kG16MaxStages = 12;
-constexpr int kG16Seg = 8;          // k blocks that one accumulation runs over where y is fp32
+constexpr int kG16Seg = 8;          // k blocks that one accumulation runs over where y is fp32 or K long
 constexpr int kG16EpiWarps = 12;  // three to a lane quarter of tensor memory
 constexpr int kG16Threads = (2 + kG16EpiWarps) * 32;
 constexpr uint32_t kG16WaitPolls = 1u << 18;  // sleeping polls of up to 10 us: a bound of seconds
@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kG16Threads, 1)
       const int n = ti.n0 + q * 32 + lane;
       if constexpr (kSeg) {
         // The tensor core's fp32 additions truncate: after 128 steps of k a sum is
-        // 1.9e-6 too small, which a 16-bit result does not see and an fp32 one
-        // does.  So here an accumulation runs over 512 inputs, and the segments
+        // 1.9e-6 too small, which an fp32 result shows, and a 16-bit one after many
+        // more.  So here an accumulation runs over 512 inputs, and the segments
         // are added in registers (K = 2048: 4e-7).
         static_assert(!kGrouped && !kCanFlip, "weights on M");
         constexpr int kB = (kNT + kStep - 1) / kStep;

@@ -117,7 +117,9 @@ static moe_status linear_gemm(Gemm16Args &a, const void *x, int64_t ldx, const v
   gemm16_plan<kGated, kMats, kNT, kF16, kSegments>(a, d);
   const int64_t tiles = (int64_t)a.nfb * ((a.rows + a.nt - 1) / a.nt);
   const int grid = a.splits > 1 ? (int)tiles * a.splits : (int)(tiles < d.sms ? tiles : d.sms);
-  if constexpr (kSegments) {  // up to two thirds of the rows: fewer sums in registers (5 % faster there; only the gated kernel spills, 28 bytes)
+  if constexpr (kSegments) {
+    // up to two thirds of the rows: fewer sums in registers (5 % faster there; of
+    // these kernels only the gated one spills, 28 bytes a thread)
     constexpr int kFew = 128 / kMats;
     if (a.nt <= kFew) return gemm16_launch<false, kGated, kMats, kFew, kF16, true>(a, grid, wm, x64, x16, d.dev, s);
   }

@@ -598,3 +598,68 @@ def test_bits_of_bf16_in_integer_tensors():
     y = torch.empty_like(want)
     moe.moe_decode_layer_bf16(desc, x.view(torch.uint16), 2, y.view(torch.int16), workspace(layer, 3, 2, 0), logits=lg)
     assert torch.equal(y, want)
+
+
+# the limits that the header names: 16 tokens up to H = 5120, one token's x up to 166,000 bytes, F = 2^20, 256 rows
+@pytest.mark.parametrize("T,E,k,H,F,shared", [
+    (16, 8, 4, 5120, 128, "gated"), (16, 16, 15, 5120, 64, "one"), (1, 2, 1, 82944, 64, "none"),
+    (1, 1, 1, 64, 1 << 20, "none"), (2, 2, 2, 64, 1 << 18, "one"), (16, 256, 15, 64, 64, "one")])
+def test_decode_layer_at_its_limits(T, E, k, H, F, shared):
+    check_decode(5, T, E, k, H, F, shared, True, True)
+
+
+@pytest.mark.parametrize("T", [3, 16])
+def test_decode_nan_token_leaves_the_others(T):
+    """A token of NaN (the padding of a batch) makes its own output NaN and no other's anything else."""
+    layer = Layer16(220, 33, 256, 128)
+    gen = torch.Generator(device="cuda").manual_seed(221)
+    x, wr, gate = normal(gen, (T, 256), 1.0), normal(gen, (32, 256), 0.06), normal(gen, (256,), 0.06)
+    y0 = run_decode(layer, x, 4, 1, wr=wr, gate=gate)[0]
+    x[1] = float("nan")
+    y1 = run_decode(layer, x, 4, 1, wr=wr, gate=gate)[0]
+    keep = torch.arange(T, device="cuda") != 1
+    assert torch.equal(y0[keep], y1[keep]) and torch.isnan(y1[1]).all()
+    assert moe.moe_device_error() == 0
+
+
+def test_a_server_s_step_on_three_streams_at_once():
+    """Decode layer, linears and grouped FFN in one graph per stream, each with its own workspaces, replayed at once:
+    the same bits as one after another."""
+    E, k, H, F = 64, 6, 512, 256
+    layer = Layer16(230, E + 1, H, F)
+
+    def state(seed):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        empty = lambda *shape: torch.empty(shape, dtype=BF, device="cuda")
+        offsets = torch.tensor([700 * i // (E + 1) for i in range(E + 2)], dtype=torch.int32, device="cuda")
+        return dict(x=normal(gen, (7, H), 1.0), wr=normal(gen, (E, H), H ** -0.5), ws=workspace(layer, 7, k, 1), y=empty(7, H),
+                    gx=normal(gen, (700, H), 1.0), off=offsets, gy=empty(700, H), lw=normal(gen, (2048, H), 0.05),
+                    gws=empty(700, F), ly=empty(700, 2048), ly2=empty(7, 2048))
+
+    def step(s):
+        moe.moe_decode_layer_bf16(layer.desc, s["x"], k, s["y"], s["ws"], wr=s["wr"], shared=1)
+        moe.moe_linear(s["y"], s["lw"], s["ly2"])
+        moe.moe_ffn_grouped_prefill_bf16(layer.desc, s["gx"], s["off"], s["gy"], s["gws"])
+        moe.moe_linear(s["gy"], s["lw"], s["ly"], act=moe.MOE_ACT_GELU)
+        moe.moe_decode_layer_bf16(layer.desc, s["y"], k, s["x"], s["ws"], wr=s["wr"], shared=1)
+
+    alone, at_once = [state(i) for i in range(3)], [state(i) for i in range(3)]
+    for s in alone:
+        for _ in range(6):
+            step(s)
+            torch.cuda.synchronize()
+    streams, graphs = [torch.cuda.Stream() for _ in range(3)], []
+    for s, q in zip(at_once, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=q):
+            for _ in range(3):
+                step(s)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for g, q in zip(graphs, streams):
+            with torch.cuda.stream(q):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(alone, at_once):
+        assert all(torch.equal(a[n], b[n]) for n in ("x", "y", "gy", "ly", "ly2"))
+    assert moe.moe_device_error() == 0
