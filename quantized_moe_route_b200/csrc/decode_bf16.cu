@@ -115,12 +115,12 @@ __device__ __forceinline__ void ld_relaxed_b128(const ulonglong2 *p, ulonglong2 
                : "memory");
 }
 // What 24 bits of a value leave beside its upper 16: hi, the value's upper half in
-// place, next, the next 8 bits in byte `at` of r.  An infinity (inf - inf is NaN)
-// leaves 1 of its sign: its products then agree in sign with those of the upper
-// half, or are as infinite, so no sum of the two halves is inf - inf.
+// place, next, the next 8 bits in byte `at` of r.  An infinity, less the largest
+// finite value, leaves itself: its products then are as infinite as the upper
+// half's and of their sign, so no sum of the two halves is inf - inf.
 __device__ __forceinline__ float b16_rest(uint32_t hi, uint32_t r, int at) {
-  const float rest = __uint_as_float(__byte_perm(hi, r, 0x3200 | (4 + at) << 4)) - __uint_as_float(hi);
-  return rest == rest ? rest : copysignf(1.0f, __uint_as_float(hi));
+  const float most = 3.4028234663852886e38f, finite = fmaxf(fminf(__uint_as_float(hi), most), -most);
+  return __uint_as_float(__byte_perm(hi, r, 0x3200 | (4 + at) << 4)) - finite;
 }
 // the n-th set bit of m (n < popc(m))
 __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
