@@ -565,7 +565,10 @@ typedef enum {
  *   gated = 1:  y = act(g) * u + residual, (g, u) = x w^T + bias,
  *               rows = 2N: rows [0, N) of w and bias give g, [N, 2N) give u
  * Products and sums are fp32 in an order fixed by the sizes (the same call
- * gives the same bits), the epilogue is fp32, and y is rounded once.
+ * gives the same bits), the epilogue is fp32, and y is rounded once.  The tensor
+ * core's additions truncate, so sums run in segments of 512 inputs (8192 up to
+ * 16 rows) where y is fp32 or K is above 2^15 (f16) or 2^18 (bf16); below, a sum of
+ * one sign may be 6e-9 K of its value too small before y's own rounding.
  * x, w, bias [rows] and residual [T][N] are of `dtype` (MOE_BF16 or MOE_F16),
  * y [T][N] of `y_dtype` (`dtype` or MOE_F32); bias and residual may be NULL.
  * ldx, ldw, ldr, ldy: elements from one row to the next, at least the row's
@@ -574,10 +577,13 @@ typedef enum {
  * y may be the residual itself (same address, type and row stride); beyond
  * that no output may overlap an input.
  * Requirements: x and w 16-byte aligned, ldx % 8 == 0 and ldw % 8 == 0, N <=
- * 2^29, T and K <= 2^30, row strides up to 2^38; otherwise any T, N, K.  T == 0 or N == 0 is a no-op.
- * No workspace.  Errors: INVALID_ARG (null, a negative size, K == 0, an unknown type
- * or activation, a row stride below its row's length, misalignment, y at x, w
- * or bias), UNSUPPORTED_SHAPE, CUDA.  A wait on the device that runs out (it
+ * 2^29, T and K <= 2^30, row strides up to 2^38; otherwise any T, N, K.
+ * T == 0 or N == 0 is a no-op.  Infinities and NaN in a row of x, of w or in
+ * bias go through sums and every activation as in fp32 arithmetic, and reach
+ * no other row's or output's results.
+ * No workspace.  Errors: INVALID_ARG (null, a negative size, K == 0, an unknown
+ * type or activation, a row stride below its row's length, misalignment, y at
+ * x, w or bias), UNSUPPORTED_SHAPE, CUDA.  A wait on the device that runs out (it
  * cannot in a sound call) raises MOE_DEVERR_PREFILL_WAIT.
  */
 MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void *w, int64_t ldw, int T, int N,
@@ -612,10 +618,13 @@ typedef struct {
  * x, y bf16 [T][H].  logits: the input when wr is NULL, else an optional
  * output; idx [T][k], w [T][k]: optional outputs (both or neither).  y may be
  * the residual itself; beyond that no output may overlap an input.
- * Each selected expert's weights are read once per call whatever the number
- * of tokens routed to it; sums are fp32 in a fixed order; h enters the down
- * projection with 16 significant bits (the int4 layer rounds it to bf16's 8).  Source: the passages of moe_decode_layer_w4a16_router; the gate
- * on the shared expert is the Qwen3.5-MoE backbone's.
+ * Each selected expert's gate and up weights are read once per call whatever
+ * the number of tokens routed to it, its down weights once for every four of
+ * its tokens (after the first time as a rule from L2); sums are fp32 in a fixed
+ * order; h enters the down projection with 16 significant bits (the int4 layer
+ * rounds it to bf16's 8).  A token of NaN leaves the others' outputs as they
+ * are.  Source: the passages of moe_decode_layer_w4a16_router; the gate on the
+ * shared expert is the Qwen3.5-MoE backbone's.
  * Workspace: moe_decode_layer_bf16_workspace_bytes(T, k, shared, E, H, F) (E =
  * layer->E) bytes, 16-byte aligned, zero-filled before its first use,
  * reusable by stream-ordered calls and replayed graphs; calls that share a
@@ -624,7 +633,8 @@ typedef struct {
  * Limits: 0 <= T <= 16, T * (k + shared) <= 256, 1 <= k <= min(Er, 32), k +
  * shared <= 32, E <= 1024, H % 64 == 0, F % 64 == 0, F <= 2^20, and the T rows
  * of x have to fit in shared memory beside the weight stages: T * (2 H + 64)
- * <= 166,000 bytes (16 tokens up to H = 5120).  Pointers to bf16 16-byte aligned.  T == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * <= 166,000 bytes (16 tokens up to H = 5120).  Pointers to bf16 16-byte
+ * aligned.  T == 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
  * WORKSPACE, CUDA.  A wait on the device that runs out raises
  * MOE_DEVERR_DECODE_H_WAIT or MOE_DEVERR_DECODE_ROUTER_WAIT.
  */
