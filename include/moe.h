@@ -566,9 +566,9 @@ typedef enum {
  *               rows = 2N: rows [0, N) of w and bias give g, [N, 2N) give u
  * Products and sums are fp32 in an order fixed by the sizes (the same call
  * gives the same bits), the epilogue is fp32, and y is rounded once.  The tensor
- * core's additions truncate, so sums run in segments of 512 inputs (8192 up to
- * 16 rows) where y is fp32 or K is above 2^15 (f16) or 2^18 (bf16); below, a sum of
- * one sign may be 6e-9 K of its value too small before y's own rounding.
+ * core's additions truncate, so sums run in segments of at most 512 inputs where
+ * y is fp32, T <= 16, or K is above 2^15 (f16) or 2^18 (bf16); elsewhere a sum
+ * may be 6e-9 K of its value too small before y's own rounding.
  * x, w, bias [rows] and residual [T][N] are of `dtype` (MOE_BF16 or MOE_F16),
  * y [T][N] of `y_dtype` (`dtype` or MOE_F32); bias and residual may be NULL.
  * ldx, ldw, ldr, ldy: elements from one row to the next, at least the row's

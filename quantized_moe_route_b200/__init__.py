@@ -12,6 +12,7 @@ The library must be built (``python -m quantized_moe_route_b200.build`` or
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -494,7 +495,9 @@ def make_bf16_layer(E, H, F, gate_up, down) -> moe_bf16_layer:
     for t, rows, cols in ((gate_up, 2 * F, H), (down, H, F)):
         if t.dtype not in _BF16 or not t.is_contiguous():
             _refuse("make_bf16_layer: weights of another type, or not contiguous")
-        if t.numel() < E * rows * cols or (t.dim() > 1 and t.shape[-1] != cols) or (t.dim() > 2 and t.shape[-2] != rows):
+        # an expert's elements are the last dimensions' ([2F][H], or [2][F][H]), unless rows or elements are counted through
+        last = [math.prod(t.shape[d:]) for d in range(1, t.dim())]
+        if t.numel() < E * rows * cols or (last and last[-1] != cols) or (len(last) > 1 and rows * cols not in last):
             _refuse("make_bf16_layer: weights of another size")
     if gate_up.get_device() < 0 or down.get_device() != gate_up.get_device():
         _refuse("make_bf16_layer: weights must be on one CUDA device")

@@ -167,7 +167,9 @@ extern "C" MOE_API moe_status moe_linear(const void *x, int64_t ldx, const void 
   if (!device_info(&d)) return MOE_ERR_CUDA;
   // Sums in segments where the tensor core's truncating additions would show:
   // they leave a sum 6e-9 K too small (K = 32768: 1.9e-4, two fifths of half a
-  // step of f16; K = 2^18: 1.6e-3, two fifths of half a step of bf16).
+  // step of f16; K = 2^18: 1.6e-3, two fifths of half a step of bf16).  It costs
+  // time only where rows are many (f16, 2048 x 40960: 2048 rows 273 -> 374 us, 300
+  // rows 71 -> 73, 40 rows 46.3 -> 46.8).
   const bool segments = a.y_f32 || K > (dtype == MOE_F16 ? 1 << 15 : 1 << 18);
   const bool f16 = dtype == MOE_F16, stream_w = linear_streams(T, N, K, gated, d.sms);
 #define MOE_LINEAR(GATED, F16)                                                        \

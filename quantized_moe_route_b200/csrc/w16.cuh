@@ -18,8 +18,8 @@ __device__ __forceinline__ float sigmoid_f32(float v) { return __fdividef(1.0f, 
 // GELU is v times the normal distribution's Phi, and the lower tail is computed
 // for itself, Phi(-a) = exp(-a^2 / 2) t P(t), t = 1 / (1 + 0.32 a): a relative
 // error of 2^-20.3 for every a >= 0 (P of degree 7 is this file's own minimax fit
-// of exp(a^2 / 2) Phi(-a) / t over 0 <= a <= 40, where (1 + erf) / 2 is off by a
-// tenth at a = 5).  In both GELUs the rounded argument of exp adds its own
+// of exp(a^2 / 2) Phi(-a) / t over 0 <= a <= 40, where (1 + erff) / 2 is 6 %
+// off at a = 5).  In both GELUs the rounded argument of exp adds its own
 // magnitude in ulps: 2^-17 at v = -9.
 template <bool kExact = false>
 __device__ __forceinline__ float activate(float v, int act) {

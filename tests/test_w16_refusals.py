@@ -235,3 +235,14 @@ def test_linear_binding_refuses_sizes_past_32_bits():
             with pytest.raises(moe.MoeError) as ei:
                 moe.moe_linear(wide(*x), wide(*w), wide(*y))
             assert ei.value.status == SHAPE, (x, w, y)
+
+
+def test_make_bf16_layer_takes_gate_and_up_as_a_dimension():
+    bf = torch.bfloat16
+    gu, dn = torch.zeros(4, 2, 64, 192, dtype=bf), torch.zeros(4, 192, 64, dtype=bf)
+    for a in (gu, gu.view(8, 64, 192).view(4, 2, 64, 192), gu.unsqueeze(0)):
+        assert "one CUDA device" in refusal(moe.make_bf16_layer, 4, 192, 64, a, dn)
+    for a in (gu.view(4, 4, 32, 192), gu.view(4, 2, 192, 64)):
+        want = "one CUDA device" if a.shape[-1] == 192 else "another size"
+        assert want in refusal(moe.make_bf16_layer, 4, 192, 64, a, dn)
+    assert "another size" in refusal(moe.make_bf16_layer, 4, 192, 64, torch.zeros(4, 3, 64, 192, dtype=bf), dn)
